@@ -98,7 +98,11 @@ typedef enum slra_status {
 typedef enum slra_out_dtype { SLRA_OUT_F32 = 0, SLRA_OUT_BF16 = 1 } slra_out_dtype;
 
 /* Element type of a tensor descriptor. */
-typedef enum slra_dtype { SLRA_DTYPE_BF16 = 0, SLRA_DTYPE_F32 = 1 } slra_dtype;
+typedef enum slra_dtype {
+    SLRA_DTYPE_BF16 = 0,
+    SLRA_DTYPE_F32 = 1,
+    SLRA_DTYPE_F16 = 2 /* the operators around the attention (slra_residual_norm, slra_qk_rope) only */
+} slra_dtype;
 
 /*
  * A [B][L][Hh][D] device tensor (batch, token, head, head dimension): `data` points at element
@@ -493,6 +497,176 @@ SLRA_API slra_status slra_lowrank_summary_noalloc(const slra_problem* p, const v
  * Like the entry point itself, this has no counterpart in the method's sources.
  */
 SLRA_API slra_status slra_noalloc_device_status(slra_stream_t stream, int32_t* status);
+
+/* ---- Operators around the attention in a transformer block ------------------------------------ */
+
+/* Norm over a row's C channels: none, x / rms(x), or (x - mean) / std. */
+typedef enum slra_norm { SLRA_NORM_NONE = 0, SLRA_NORM_RMS = 1, SLRA_NORM_LAYER = 2 } slra_norm;
+
+/*
+ * The end of one block and the start of the next, row by row over [batch][tokens][channels] tensors:
+ *   yh    = y, or y rsqrt(mean(y^2) + post_eps) post_weight   (post_norm = SLRA_NORM_RMS)
+ *   sum   = residual_scale x + gate yh                        (sum = x where there is no y)
+ *   x_out = sum
+ *   h     = n (1 + scale) + shift, n = (sum - m) rsqrt(mean((sum - m)^2) + eps) weight + bias with
+ *           m = mean(sum) (SLRA_NORM_LAYER) or 0 (SLRA_NORM_RMS)
+ * in fp32, each output rounded once; h is the norm of the unrounded sum.
+ *
+ * Fill it with slra_residual_norm_init, then adjust:
+ *   batch, tokens, channels  channels a multiple of 8, at most 8192; batch * tokens below 2^31.
+ *   groups                   modulation rows of a sample (default 1): token l uses row
+ *                            l / (tokens / groups), so 1 is per sample, the number of latent frames per
+ *                            frame, tokens per token.  Must divide tokens.
+ *   norm                     of h: LAYER (default), RMS, or NONE: h is not computed (h, dh NULL).
+ *   post_norm                of y: NONE (default) or RMS.
+ *   stream_dtype             of x, x_out, dx_out, dx: bf16 (default), f16, or f32 with any block_dtype;
+ *   block_dtype              of y, h, dh, dy: bf16 (default), f16, f32; equal to stream_dtype unless that
+ *                            is f32.
+ *   mod_dtype, weight_dtype  of gate, scale, shift / of weight, bias, post_weight (default f32).
+ *   eps, post_eps            positive (default 1e-6).
+ *   residual_scale           default 1; must be 1 where there is no y.
+ *   *_strides                element strides (batch, token) of the row tensors, all zero (default) =
+ *                            contiguous, else positive multiples of 16 bytes below 2^36; a backward's
+ *                            dx_out and dh use x_out_strides and h_strides.
+ *   gate/scale/shift_strides element strides (batch, modulation row) of [batch][groups][channels]
+ *                            vectors, multiples of 16 bytes; 0 broadcasts; -1 (default) = contiguous.
+ *   gate, scale, shift       device vectors, NULL = 1, 0, 0.  A gate needs y.
+ *   weight, bias             device vectors [channels] of the norm, NULL = 1, 0 (bias: LAYER only).
+ *   post_weight              device vector [channels] (with post_norm), NULL = 1.
+ *   dgate, dscale, dshift    backward outputs, fp32 [batch][groups][channels] contiguous (a vector that
+ *                            is broadcast still gets its gradient per sample and modulation row), NULL:
+ *                            not wanted; only where the vector itself is given.
+ *   dweight, dbias,          backward outputs, fp32 [channels], NULL: not wanted; only where the vector
+ *   dpost_weight             itself is given.
+ * All pointers 16-B aligned.
+ */
+typedef struct slra_residual_norm {
+    int64_t batch, tokens, channels, groups;
+    int32_t norm, post_norm;
+    int32_t stream_dtype, block_dtype, mod_dtype, weight_dtype;
+    float eps, post_eps, residual_scale;
+    int64_t x_strides[2], y_strides[2], x_out_strides[2], h_strides[2], dx_strides[2], dy_strides[2];
+    int64_t gate_strides[2], scale_strides[2], shift_strides[2];
+    const void *gate, *scale, *shift, *weight, *bias, *post_weight;
+    float *dgate, *dscale, *dshift, *dweight, *dbias, *dpost_weight;
+} slra_residual_norm;
+
+/* Fill *p with the sizes and the defaults above.  Returns SLRA_ERR_INVALID_ARG if p is NULL. */
+SLRA_API slra_status slra_residual_norm_init(slra_residual_norm* p, int64_t batch, int64_t tokens, int64_t channels);
+
+/*
+ * The operator above.  y NULL: h = norm of x alone, x_out must be NULL.  h NULL with SLRA_NORM_NONE.
+ * x_out may be x and h may be y exactly (same address, strides and type); outputs may not overlap
+ * anything else.  One launch on `stream`, no workspace.
+ */
+SLRA_API slra_status slra_residual_norm_fwd(const slra_residual_norm* p, const void* x, const void* y, void* x_out,
+                                            void* h, slra_stream_t stream);
+
+/* Workspace bytes of slra_residual_norm_bwd for p (sums over a part of a call's tokens); 0 if p is
+ * invalid.  No GPU access. */
+SLRA_API size_t slra_residual_norm_bwd_workspace_bytes(const slra_residual_norm* p);
+
+/*
+ * Gradients of sum(dx_out x_out) + sum(dh h) for x, y and the vectors whose outputs p names.  x, y and p
+ * are the forward's; nothing of the forward is kept.
+ *   dx_out     stream type, the gradient reaching x_out (the residual stream behind); NULL = zero.
+ *   dh         block type, the gradient reaching h; NULL exactly where p->norm is NONE.
+ *   dx, dy     stream / block type; dy NULL exactly where y is.  dx may be dx_out and dy may be dh
+ *              exactly; outputs may not overlap anything else.
+ *   workspace  at least slra_residual_norm_bwd_workspace_bytes(p) bytes, 256-B aligned, or NULL
+ *              (allocated and freed on `stream`, see the conventions).
+ * Sums over tokens are joined in a fixed order: deterministic.  One or two launches on `stream`.
+ */
+SLRA_API slra_status slra_residual_norm_bwd(const slra_residual_norm* p, const void* x, const void* y,
+                                            const void* dx_out, const void* dh, void* dx, void* dy, void* workspace,
+                                            size_t workspace_bytes, slra_stream_t stream);
+
+/* Norm of q and k before the rotation: none, over each head's D elements, or over all heads of a token. */
+typedef enum slra_qk_norm { SLRA_QK_NORM_NONE = 0, SLRA_QK_NORM_HEAD = 1, SLRA_QK_NORM_TOKEN = 2 } slra_qk_norm;
+/* Which elements of a head form rotary pair j: (2j, 2j + 1), or (j, j + D / 2). */
+typedef enum slra_rope_pairing { SLRA_ROPE_INTERLEAVED = 0, SLRA_ROPE_HALVES = 1 } slra_rope_pairing;
+/* Frequencies: each axis its own schedule theta^(-m / n_axis) over its n_axis pairs (the attention's), or
+ * one schedule theta^(-j / n) over all n rotated pairs, shared out to the axes. */
+typedef enum slra_rope_schedule { SLRA_ROPE_PER_AXIS = 0, SLRA_ROPE_SHARED = 1 } slra_rope_schedule;
+
+/*
+ * RMS norm of q and k and their rotation by positions along (t, h, w), both optional:
+ *   out = R(p) (x rsqrt(mean(x^2) + eps) w), pair (a, b) -> (a cos - b sin, a sin + b cos) at the angle
+ *   p[axis_j] omega_j; in fp32 (angles in double), rounded once.
+ * The attention entry points rotate q and k themselves: give them the norm alone (rotate = 0).  The
+ * rotation serves attention that does not (dense layers, cached keys).
+ *
+ * Fill it with slra_qk_rope_init, then adjust:
+ *   batch, tokens, heads,    q is [batch][tokens][heads][head_dim], k the same with kv_heads (0: no k).
+ *   kv_heads, head_dim       head_dim a multiple of 8, at most 256; with g = head_dim / 8 rounded up to
+ *                            a power of two, (heads + kv_heads) g at most 2048; batch * tokens below 2^31.
+ *   T, H, W, first_token     grid positions (default; all 1): token n of every sample sits at place
+ *                            first_token + n of the row-major t, h, w grid, which must hold it.
+ *   positions,               or listed ones: device int32 [batch][tokens][3] (t, h, w), 4-B aligned,
+ *   positions_stride         samples positions_stride elements apart (default 0: one list for all
+ *                            samples, else at least 3 * tokens).  T, H, W and first_token are then unused.
+ *   pos_offset               added to every position, within +-2^31.
+ *   rope_split               rotary pairs per (t, h, w), grouped in that order; all zero (default) =
+ *                            c - 2 floor(c / 3), floor(c / 3), floor(c / 3) with c = head_dim / 2.  Their
+ *                            sum may be below c: later pairs are not rotated.
+ *   theta                    rotary base (default 10000).
+ *   norm                     SLRA_QK_NORM_* (default NONE); eps positive (default 1e-6).
+ *   rotate                   1 (default) or 0.
+ *   pairing, schedule        SLRA_ROPE_* (default INTERLEAVED, PER_AXIS: the attention's).
+ *   x_dtype                  of q, k, dq, dk: bf16 (default), f16, f32.
+ *   out_dtype                of out_q, out_k, dout_q, dout_k: x_dtype or f32 (default bf16).
+ *   weight_dtype             of wq, wk (default f32).
+ *   wq, wk                   device vectors of the norm: [head_dim] (HEAD) or [heads * head_dim] (TOKEN),
+ *                            16-B aligned; NULL = 1.
+ *   dwq, dwk                 backward outputs, fp32 of wq's, wk's size, NULL: not wanted.  16-B aligned;
+ *                            only where the weight itself is given.
+ *   *_strides                element strides (batch, token, head), all zero (default) = contiguous, else
+ *                            positive multiples of 16 bytes below 2^36 (e.g. views of a fused QKV
+ *                            buffer); a backward's dout_q, dout_k use out_q_strides, out_k_strides.
+ */
+typedef struct slra_qk_rope {
+    int64_t batch, tokens, heads, kv_heads, head_dim;
+    int64_t T, H, W, first_token;
+    int64_t pos_offset[3], rope_split[3];
+    double theta;
+    int32_t norm, rotate, pairing, schedule;
+    int32_t x_dtype, out_dtype, weight_dtype;
+    float eps;
+    int64_t q_strides[3], k_strides[3], out_q_strides[3], out_k_strides[3], dq_strides[3], dk_strides[3];
+    const int32_t* positions;
+    int64_t positions_stride;
+    const void *wq, *wk;
+    float *dwq, *dwk;
+} slra_qk_rope;
+
+/* Fill *p with the sizes (no k, a 1 x 1 x tokens grid) and the defaults above.  Returns
+ * SLRA_ERR_INVALID_ARG if p is NULL. */
+SLRA_API slra_status slra_qk_rope_init(slra_qk_rope* p, int64_t batch, int64_t tokens, int64_t heads,
+                                       int64_t head_dim);
+
+/*
+ * The operator above; k and out_k NULL exactly where kv_heads is 0.  out_q may be q and out_k may be k
+ * exactly (same address, strides and type); outputs may not overlap anything else (interleaved views of
+ * one buffer do not overlap).  One launch on `stream`, no workspace.
+ */
+SLRA_API slra_status slra_qk_rope_fwd(const slra_qk_rope* p, const void* q, const void* k, void* out_q, void* out_k,
+                                      slra_stream_t stream);
+
+/* Workspace bytes of slra_qk_rope_bwd for p (the weights' sums over a part of the tokens); 0 if p is
+ * invalid.  No GPU access. */
+SLRA_API size_t slra_qk_rope_bwd_workspace_bytes(const slra_qk_rope* p);
+
+/*
+ * Gradients of sum(dout_q out_q) + sum(dout_k out_k) for q, k and the weights.  q, k and p are the
+ * forward's (out_dtype: that of dout; q and k are not read, and may be NULL, without a norm).
+ *   dq, dk     x_dtype; may be dout_q, dout_k exactly where that is x_dtype; else no overlap.
+ *   workspace  at least slra_qk_rope_bwd_workspace_bytes(p) bytes, 256-B aligned, or NULL (allocated and
+ *              freed on `stream`).
+ * Sums over tokens are joined in a fixed order: deterministic.  One or two launches on `stream`.
+ */
+SLRA_API slra_status slra_qk_rope_bwd(const slra_qk_rope* p, const void* q, const void* k, const void* dout_q,
+                                      const void* dout_k, void* dq, void* dk, void* workspace,
+                                      size_t workspace_bytes, slra_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -267,4 +267,74 @@ cudaError_t launch_gate_prep(const float* dout, const float* os, const float* ol
 cudaError_t launch_gate_final(const __nv_bfloat16* q, const float* dlogit, const float* gate_w, const Geom& g,
                               float* dq, float* part, float* dgw, float* dgb, cudaStream_t st);
 
+// ---- operators around the attention: rows of tokens (residual_norm.cu, qk_rope.cu) --------------
+constexpr int kSMs = 148;
+constexpr int kMaxWorkers = 32768;  // teams of threads that share a call's rows, at most
+constexpr int kNormNone = 0, kNormRms = 1, kNormLayer = 2;  // slra_norm
+
+// How a call's rows are shared out: `V` vectors of eight elements a thread, `team` threads a row,
+// `blocks` blocks of `threads` threads, `workers` teams in all.
+struct RowPlan {
+    int V, team, threads, blocks, workers;
+};
+
+struct RowTensor {  // [B][L][C], C contiguous; element strides of batch and token
+    void* p;
+    long long b, l;
+};
+struct ModTensor {  // [B][groups][C], C contiguous; element strides of batch and group (0 broadcasts)
+    const void* p;
+    long long b, f;
+};
+struct ResidualNormArgs {
+    RowTensor x, y, x_out, h;      // forward; y.p null: no residual
+    RowTensor dx_out, dh, dx, dy;  // backward; dx_out.p null: zero
+    ModTensor gate, scale, shift;  // null: 1, 0, 0
+    const void *weight, *bias, *post_weight;  // [C]; null: 1, 0, 1
+    float *dgate, *dscale, *dshift;           // [B][groups][C], null: not wanted
+    float *dweight, *dbias, *dpost;           // [C], null: not wanted
+    float* part;   // [2 * workers][3][C]: sums over a part of a modulation row (null: none is wanted)
+    float* wpart;  // [workers][3][C]: the weights' sums (null: none is wanted)
+    long long rows;
+    int tokens, channels, groups, per;  // per: tokens of a modulation row
+    int stream_dtype, block_dtype, mod_dtype, w_dtype;
+    int norm, post;
+    float eps, post_eps, rs;
+    int team, workers, stages, wsum_shared;  // set by the launcher
+};
+RowPlan residual_norm_plan(long long rows, int channels, bool backward);
+cudaError_t launch_residual_norm(const ResidualNormArgs& a, bool backward, cudaStream_t st);
+
+constexpr int kRopeMaxPairs = 128;  // head_dim <= 256
+constexpr int kQkNormNone = 0, kQkNormHead = 1, kQkNormToken = 2;  // slra_qk_norm
+
+// One of q, k: its head vectors [B][L][heads][D], their counterparts and the norm's weight.
+struct RopeSide {
+    const void* x;
+    const void* d;  // backward: gradient of the output
+    void* out;      // forward: the output; backward: the gradient of x
+    Strides sx, sd, so;
+    const void* weight;  // [D] (norm per head) or [heads * D]; null: 1
+    float* dweight;      // backward; null: not wanted
+    int heads;
+};
+struct QkRopeArgs {
+    RopeSide side[2];        // q, k (k: zero heads when absent)
+    const int32_t* positions;  // [B or 1][L][3], null: grid
+    long long positions_b;     // elements between samples
+    long long rows, first;     // B * L; first token of the grid
+    int tokens, head_dim;
+    int H, W;                  // grid (t is unbounded here)
+    long long offset[3];
+    int rotate, halves, norm;
+    int x_dtype, out_dtype, w_dtype;
+    float eps;
+    float* part;  // [workers][sum of the weights' elements]: the weights' sums (null: none is wanted)
+    double turns[kRopeMaxPairs];   // omega / (2 pi) per pair, 0 for a pair that is not rotated
+    uint8_t axis[kRopeMaxPairs];
+    int group, team, workers, stages;  // set by the launcher
+};
+RowPlan qk_rope_plan(long long rows, int head_dim, int heads, bool backward);
+cudaError_t launch_qk_rope(const QkRopeArgs& a, bool backward, cudaStream_t st);
+
 }  // namespace slra

@@ -8,7 +8,9 @@ there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+from collections import namedtuple
 from dataclasses import dataclass, field
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -21,9 +23,13 @@ OUT_F32, OUT_BF16 = 0, 1
 BRANCH_SPARSE, BRANCH_LOWRANK, BRANCH_BOTH = 1, 2, 3
 DEBUG_UNSATISFIED_WAIT, DEBUG_SERIAL_BRANCHES = 1, 2
 ABI_VERSION = 8
-DTYPE_BF16, DTYPE_F32 = 0, 1
+DTYPE_BF16, DTYPE_F32, DTYPE_F16 = 0, 1, 2
 ACT_RELU, ACT_SILU, ACT_IDENTITY, ACT_TANH = 0, 1, 2, 3
 FUSION_SUM, FUSION_GATED = 0, 1
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
+QK_NORM_NONE, QK_NORM_HEAD, QK_NORM_TOKEN = 0, 1, 2
+ROPE_INTERLEAVED, ROPE_HALVES = 0, 1
+ROPE_PER_AXIS, ROPE_SHARED = 0, 1
 
 # Every symbol include/slra.h declares.
 EXPORTS = ("slra_abi_version", "slra_status_string", "slra_problem_init", "slra_validate", "slra_keep_count",
@@ -32,7 +38,10 @@ EXPORTS = ("slra_abi_version", "slra_status_string", "slra_problem_init", "slra_
            "slra_workspace_layout", "slra_host_io_bytes", "slra_host_pipeline_groups",
            "slra_attn_fwd_host",
            "slra_select_blocks", "slra_lowrank_summary", "slra_device_status", "slra_lowrank_summary_noalloc",
-           "slra_noalloc_device_status", "slra_attn_fwd_train", "slra_attn_bwd_saved")
+           "slra_noalloc_device_status", "slra_attn_fwd_train", "slra_attn_bwd_saved",
+           "slra_residual_norm_init", "slra_residual_norm_fwd", "slra_residual_norm_bwd_workspace_bytes",
+           "slra_residual_norm_bwd", "slra_qk_rope_init", "slra_qk_rope_fwd", "slra_qk_rope_bwd_workspace_bytes",
+           "slra_qk_rope_bwd")
 
 
 class SlraError(RuntimeError):
@@ -65,6 +74,26 @@ class _Tensor(ctypes.Structure):
 
 class _Mat(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("D", ctypes.c_int64), ("R", ctypes.c_int64)]
+
+
+_I32, _I64, _F32, _P = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_void_p
+
+
+class _ResidualNorm(ctypes.Structure):
+    _fields_ = [(n, _I64) for n in ("batch", "tokens", "channels", "groups")] + \
+               [(n, _I32) for n in ("norm", "post_norm", "stream_dtype", "block_dtype", "mod_dtype", "weight_dtype")] + \
+               [(n, _F32) for n in ("eps", "post_eps", "residual_scale")] + \
+               [(n + "_strides", _I64 * 2) for n in ("x", "y", "x_out", "h", "dx", "dy", "gate", "scale", "shift")] + \
+               [(n, _P) for n in ("gate", "scale", "shift", "weight", "bias", "post_weight", "dgate", "dscale", "dshift",
+                                  "dweight", "dbias", "dpost_weight")]
+
+
+class _QkRope(ctypes.Structure):
+    _fields_ = [(n, _I64) for n in ("batch", "tokens", "heads", "kv_heads", "head_dim", "T", "H", "W", "first_token")] + \
+               [("pos_offset", _I64 * 3), ("rope_split", _I64 * 3), ("theta", ctypes.c_double)] + \
+               [(n, _I32) for n in ("norm", "rotate", "pairing", "schedule", "x_dtype", "out_dtype", "weight_dtype")] + \
+               [("eps", _F32)] + [(n + "_strides", _I64 * 3) for n in ("q", "k", "out_q", "out_k", "dq", "dk")] + \
+               [("positions", _P), ("positions_stride", _I64)] + [(n, _P) for n in ("wq", "wk", "dwq", "dwk")]
 
 
 class _Layout(ctypes.Structure):
@@ -122,6 +151,18 @@ def lib():
         L.slra_device_status.argtypes = [P, P, ctypes.POINTER(ctypes.c_int32)]
         L.slra_lowrank_summary_noalloc.argtypes = [PP, P, P, P, P, P, P]
         L.slra_noalloc_device_status.argtypes = [P, ctypes.POINTER(ctypes.c_int32)]
+        PN, PR = ctypes.POINTER(_ResidualNorm), ctypes.POINTER(_QkRope)
+        L.slra_residual_norm_init.argtypes = [PN, I64, I64, I64]
+        L.slra_residual_norm_fwd.argtypes = [PN, P, P, P, P, P]
+        L.slra_residual_norm_bwd.argtypes = [PN, P, P, P, P, P, P, P, S, P]
+        L.slra_qk_rope_init.argtypes = [PR, I64, I64, I64, I64]
+        L.slra_qk_rope_fwd.argtypes = [PR, P, P, P, P, P]
+        L.slra_qk_rope_bwd.argtypes = [PR, P, P, P, P, P, P, P, S, P]
+        for name, arg in (("slra_residual_norm", PN), ("slra_qk_rope", PR)):
+            f = getattr(L, name + "_bwd_workspace_bytes")
+            f.restype, f.argtypes = S, [arg]
+            for verb in ("_init", "_fwd", "_bwd"):
+                getattr(L, name + verb).restype = ctypes.c_int
         for name in ("slra_problem_init", "slra_validate", "slra_workspace_layout", "slra_attn_fwd",
                      "slra_attn_fwd_ex", "slra_sparse_fwd", "slra_lowrank_fwd", "slra_get_device_status",
                      "slra_attn_bwd", "slra_attn_bwd_saved", "slra_attn_fwd_train",
@@ -514,3 +555,364 @@ def ws_view(prob: Problem, workspace, name: str):
         n *= s
     nbytes = n * torch.empty(0, dtype=dt).element_size()
     return workspace[off:off + nbytes].view(dt).view(shape)
+
+
+# ------------------------------------------------------------- operators around the attention
+def _code(t) -> int:
+    torch = _torch()
+    dt = t.dtype
+    if dt is torch.bfloat16:
+        return DTYPE_BF16
+    if dt is torch.float32:
+        return DTYPE_F32
+    if dt is torch.float16:
+        return DTYPE_F16
+    raise ValueError(f"expected bf16, fp16 or fp32, got {dt}")
+
+
+def _torch_dtype(code):
+    torch = _torch()
+    return {DTYPE_BF16: torch.bfloat16, DTYPE_F32: torch.float32, DTYPE_F16: torch.float16}[code]
+
+
+class _Call:
+    """Runs a call with the tensors' device current, on `stream` (None: that device's current stream);
+    what it allocates then belongs to that stream."""
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        if device.type != "cuda":
+            raise ValueError(f"expected CUDA tensors, got {device}")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+        self.ctx = None
+        if stream is not None or torch.cuda.current_device() != device.index:
+            self.ctx = torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device))
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return int(_torch().cuda.current_stream().cuda_stream)
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _expect(name, t, shape, dtype, device):
+    """A CUDA tensor of this shape (and type, where one is given), its last dimension contiguous."""
+    if not t.is_cuda or t.shape != shape or (dtype is not None and t.dtype is not dtype) or \
+            (t.stride(-1) != 1 and shape[-1] != 1):
+        raise ValueError(f"{name}: expected a CUDA {'' if dtype is None else str(dtype) + ' '}tensor of shape "
+                         f"{tuple(shape)} with a contiguous last dimension, got {t.dtype} {tuple(t.shape)} strides "
+                         f"{t.stride()} on {t.device}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+def _steps(t):
+    """Strides of the dimensions before the last one, (0, ...) when contiguous; a dimension of one element
+    gets any valid stride."""
+    if t.is_contiguous():
+        return (0,) * (t.dim() - 1)
+    return tuple(st if n > 1 else 8 for st, n in zip(t.stride()[:-1], t.shape[:-1]))
+
+
+def _dense(name, t, shape, dtype, device):
+    _expect(name, t, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+
+
+@dataclass(frozen=True)
+class ResidualNorm:
+    """Sizes and options of slra_residual_norm (see include/slra.h): x, y, x_out and h are
+    [batch, tokens, channels], the modulation vectors [batch, groups, channels].  Types and strides are
+    taken from the tensors of each call."""
+    batch: int
+    tokens: int
+    channels: int
+    groups: int = 1             # modulation rows of a sample: 1, the number of frames, or tokens
+    norm: int = NORM_LAYER      # of h; NORM_NONE: x_out alone
+    post_norm: int = NORM_NONE  # of y: NORM_NONE or NORM_RMS
+    eps: float = 1e-6
+    post_eps: float = 1e-6
+    residual_scale: float = 1.0
+
+
+ResidualNormGrads = namedtuple("ResidualNormGrads",
+                               "dx dy dgate dscale dshift dweight dbias dpost_weight workspace")
+
+
+@functools.lru_cache(maxsize=256)
+def _residual_norm_template(prob: ResidualNorm) -> bytes:
+    c = _ResidualNorm()
+    _check(lib().slra_residual_norm_init(ctypes.byref(c), prob.batch, prob.tokens, prob.channels),
+           "slra_residual_norm_init")
+    c.groups, c.norm, c.post_norm = prob.groups, prob.norm, prob.post_norm
+    c.eps, c.post_eps, c.residual_scale = prob.eps, prob.post_eps, prob.residual_scale
+    return bytes(c)
+
+
+def _residual_norm_problem(prob, x, y, h, gate, scale, shift, weight, bias, post_weight):
+    """The filled C struct from the tensors; h (or dh) may be None: the block type is then y's, or x's."""
+    c = _ResidualNorm.from_buffer_copy(_residual_norm_template(prob))
+    row = (prob.batch, prob.tokens, prob.channels)
+    _expect("x", x, row, None, x.device)
+    c.stream_dtype = _code(x)
+    c.x_strides[:] = _steps(x)
+    block = y if y is not None else h if h is not None else x
+    c.block_dtype = _code(block)
+    if y is not None:
+        _expect("y", y, row, None, x.device)
+        c.y_strides[:] = _steps(y)
+    dtype = None
+    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
+        if t is not None:
+            _expect(name, t, (prob.batch, prob.groups, prob.channels), dtype, x.device)
+            dtype = t.dtype
+            c.mod_dtype = _code(t)
+            setattr(c, name, t.data_ptr())
+            if not t.is_contiguous():
+                getattr(c, name + "_strides")[:] = (t.stride(0) if prob.batch > 1 else 0,
+                                                    t.stride(1) if prob.groups > 1 else 0)
+    dtype = None
+    for name, t in (("weight", weight), ("bias", bias), ("post_weight", post_weight)):
+        if t is not None:
+            _dense(name, t, (prob.channels,), dtype, x.device)
+            dtype = t.dtype
+            c.weight_dtype = _code(t)
+            setattr(c, name, t.data_ptr())
+    return c, block.dtype
+
+
+def residual_norm_fwd(prob: ResidualNorm, x, y=None, gate=None, scale=None, shift=None, weight=None, bias=None,
+                      post_weight=None, x_out=None, h=None, h_dtype=None, stream=None):
+    """x_out = residual_scale x + gate post(y) and h = norm(x_out) (1 + scale) + shift in one pass
+    (slra_residual_norm_fwd).  x: the residual stream, bf16, fp16 or fp32 [batch, tokens, channels]; y: the
+    block's output (None: the norm before the first block); gate, scale, shift: [batch, groups, channels]
+    (expanded views broadcast); weight, bias, post_weight: [channels].  h gets y's type, or h_dtype (a
+    torch dtype; for a call without y, default x's).  Rows may be strided, x_out may be x and h may be y.
+    Returns (x_out, h): x itself where there is no y, None for h with NORM_NONE."""
+    torch = _torch()
+    row = (prob.batch, prob.tokens, prob.channels)
+    c, block = _residual_norm_problem(prob, x, y, h, gate, scale, shift, weight, bias, post_weight)
+    if h_dtype is not None and y is None and h is None:
+        block = h_dtype
+        c.block_dtype = _code(torch.empty(0, dtype=h_dtype))
+    with _Call(x.device, stream) as handle:
+        if y is not None:
+            if x_out is None:
+                x_out = torch.empty(row, dtype=x.dtype, device=x.device)
+            else:
+                _expect("x_out", x_out, row, x.dtype, x.device)
+                c.x_out_strides[:] = _steps(x_out)
+        elif x_out is not None:
+            raise ValueError("x_out: there is no y to add")
+        if prob.norm != NORM_NONE:
+            if h is None:
+                h = torch.empty(row, dtype=block, device=x.device)
+            else:
+                _expect("h", h, row, block, x.device)
+                c.h_strides[:] = _steps(h)
+        elif h is not None:
+            raise ValueError("h: the problem has no norm")
+        _check(lib().slra_residual_norm_fwd(ctypes.byref(c), x.data_ptr(), None if y is None else y.data_ptr(),
+                                            None if y is None else x_out.data_ptr(),
+                                            None if h is None else h.data_ptr(), handle), "slra_residual_norm_fwd")
+    return (x if y is None else x_out), h
+
+
+def residual_norm_bwd(prob: ResidualNorm, x, y=None, dh=None, dx_out=None, gate=None, scale=None, shift=None,
+                      weight=None, bias=None, post_weight=None, dx=None, dy=None, workspace=None, stream=None):
+    """Gradients of sum(dx_out x_out) + sum(dh h) (slra_residual_norm_bwd) from the forward's inputs; dh has
+    the block's type, dx_out (the gradient of the stream behind, None: zero) x's.  Every vector that is
+    given gets its gradient, in fp32: dgate, dscale, dshift [batch, groups, channels], dweight, dbias,
+    dpost_weight [channels].  dx may be dx_out and dy may be dh.  workspace: a uint8 tensor to reuse (None:
+    allocated; it comes back in the result).  Returns ResidualNormGrads, None where there is nothing."""
+    torch = _torch()
+    row, mods, dev = (prob.batch, prob.tokens, prob.channels), (prob.batch, prob.groups, prob.channels), x.device
+    c, block = _residual_norm_problem(prob, x, y, dh, gate, scale, shift, weight, bias, post_weight)
+    if dh is not None:
+        _expect("dh", dh, row, block, dev)
+        c.h_strides[:] = _steps(dh)
+    if dx_out is not None:
+        _expect("dx_out", dx_out, row, x.dtype, dev)
+        c.x_out_strides[:] = _steps(dx_out)
+    with _Call(dev, stream) as handle:
+        if dx is None:
+            dx = torch.empty(row, dtype=x.dtype, device=dev)
+        else:
+            _expect("dx", dx, row, x.dtype, dev)
+            c.dx_strides[:] = _steps(dx)
+        if y is None:
+            if dy is not None:
+                raise ValueError("dy: there is no y")
+        elif dy is None:
+            dy = torch.empty(row, dtype=block, device=dev)
+        else:
+            _expect("dy", dy, row, block, dev)
+            c.dy_strides[:] = _steps(dy)
+        out = {}
+        for name, t, shape in (("dgate", gate, mods), ("dscale", scale, mods), ("dshift", shift, mods),
+                               ("dweight", weight, mods[2:]), ("dbias", bias, mods[2:]),
+                               ("dpost_weight", post_weight, mods[2:])):
+            out[name] = None
+            if t is not None:
+                out[name] = torch.empty(shape, dtype=torch.float32, device=dev)
+                setattr(c, name, out[name].data_ptr())
+        workspace = _sums_workspace("slra_residual_norm_bwd", c, workspace, dev)
+        _check(lib().slra_residual_norm_bwd(ctypes.byref(c), x.data_ptr(), None if y is None else y.data_ptr(),
+                                            None if dx_out is None else dx_out.data_ptr(),
+                                            None if dh is None else dh.data_ptr(), dx.data_ptr(),
+                                            None if dy is None else dy.data_ptr(), workspace.data_ptr(),
+                                            workspace.numel(), handle), "slra_residual_norm_bwd")
+    return ResidualNormGrads(dx, dy, workspace=workspace, **out)
+
+
+def _sums_workspace(call, c, workspace, device):
+    """The caller's workspace, or one of the size the call needs (a problem that is refused gets a token
+    one: the call itself then says why)."""
+    if workspace is None:
+        n = getattr(lib(), call + "_workspace_bytes")(ctypes.byref(c))
+        return _torch().empty(max(n, 256), dtype=_torch().uint8, device=device)
+    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous() or \
+            workspace.element_size() != 1:
+        raise ValueError(f"workspace: expected a contiguous uint8 tensor on {device}")
+    return workspace
+
+
+@dataclass(frozen=True)
+class QkRope:
+    """Sizes and options of slra_qk_rope (see include/slra.h): q is [batch, tokens, heads, head_dim], k the
+    same with kv_heads.  Types and strides are taken from the tensors of each call."""
+    batch: int
+    tokens: int
+    heads: int
+    head_dim: int
+    kv_heads: int = 0                # 0: no k
+    grid: tuple = None               # (T, H, W) of the positions; None: (1, 1, tokens)
+    first_token: int = 0             # the grid place of token 0
+    pos_offset: tuple = (0, 0, 0)
+    rope_split: tuple = (0, 0, 0)    # pairs per axis; all 0: the default split
+    theta: float = 1e4
+    norm: int = QK_NORM_NONE
+    eps: float = 1e-6
+    rotate: bool = True
+    pairing: int = ROPE_INTERLEAVED
+    schedule: int = ROPE_PER_AXIS
+    out_dtype: int = None            # of the forward's outputs, DTYPE_*; None: q's
+
+
+QkRopeGrads = namedtuple("QkRopeGrads", "dq dk dwq dwk workspace")
+
+
+@functools.lru_cache(maxsize=256)
+def _qk_rope_template(prob: QkRope) -> bytes:
+    c = _QkRope()
+    _check(lib().slra_qk_rope_init(ctypes.byref(c), prob.batch, prob.tokens, prob.heads, prob.head_dim),
+           "slra_qk_rope_init")
+    c.kv_heads, c.first_token, c.theta = prob.kv_heads, prob.first_token, prob.theta
+    if prob.grid is not None:
+        c.T, c.H, c.W = prob.grid
+    c.pos_offset[:] = prob.pos_offset
+    c.rope_split[:] = prob.rope_split
+    c.norm, c.eps, c.rotate, c.pairing, c.schedule = prob.norm, prob.eps, int(prob.rotate), prob.pairing, prob.schedule
+    return bytes(c)
+
+
+def _qk_rope_problem(prob, wq, wk, positions, device):
+    torch = _torch()
+    c = _QkRope.from_buffer_copy(_qk_rope_template(prob))
+    dtype = None
+    for name, w, heads in (("wq", wq, prob.heads), ("wk", wk, prob.kv_heads)):
+        if w is not None:
+            _dense(name, w, ((heads if prob.norm == QK_NORM_TOKEN else 1) * prob.head_dim,), dtype, device)
+            dtype = w.dtype
+            c.weight_dtype = _code(w)
+            setattr(c, name, w.data_ptr())
+    if positions is not None:
+        if positions.dim() != 3 or positions.shape[0] not in (1, prob.batch) or \
+                (prob.tokens > 1 and positions.stride(1) != 3):
+            raise ValueError(f"positions: expected int32 [1 or {prob.batch}, {prob.tokens}, 3], every sample contiguous")
+        _expect("positions", positions, (positions.shape[0], prob.tokens, 3), torch.int32, device)
+        c.positions = positions.data_ptr()
+        c.positions_stride = positions.stride(0) if positions.shape[0] > 1 else 0
+    return c
+
+
+def qk_rope_fwd(prob: QkRope, q, k=None, wq=None, wk=None, positions=None, out_q=None, out_k=None, stream=None):
+    """QK norm and rotary positions (slra_qk_rope_fwd): q, k bf16, fp16 or fp32 (any strides with a
+    contiguous last dimension, e.g. views of a fused QKV tensor); wq, wk: the norm's weights ([head_dim], or
+    [heads * head_dim] with QK_NORM_TOKEN); positions: int32 [1 or batch, tokens, 3] in place of the grid.
+    out_q may be q and out_k may be k.  Returns (out_q, out_k); out_k is None without k."""
+    torch = _torch()
+    c = _qk_rope_problem(prob, wq, wk, positions, q.device)
+    c.x_dtype = _code(q)
+    c.out_dtype = c.x_dtype if prob.out_dtype is None else prob.out_dtype
+    out_dtype = q.dtype if prob.out_dtype is None else _torch_dtype(prob.out_dtype)
+    if (k is not None) != (prob.kv_heads > 0):
+        raise ValueError(f"k: the problem has {prob.kv_heads} key heads")
+    outs = []
+    with _Call(q.device, stream) as handle:
+        for n, t, o, heads in (("q", q, out_q, prob.heads), ("k", k, out_k, prob.kv_heads)):
+            if t is None:
+                if o is not None:
+                    raise ValueError(f"out_{n}: there is no {n}")
+                outs.append(None)
+                continue
+            shape = (prob.batch, prob.tokens, heads, prob.head_dim)
+            _expect(n, t, shape, q.dtype, q.device)
+            getattr(c, n + "_strides")[:] = _steps(t)
+            if o is None:
+                o = torch.empty(shape, dtype=out_dtype, device=q.device)
+            else:
+                _expect("out_" + n, o, shape, out_dtype, q.device)
+                getattr(c, f"out_{n}_strides")[:] = _steps(o)
+            outs.append(o)
+        _check(lib().slra_qk_rope_fwd(ctypes.byref(c), q.data_ptr(), None if k is None else k.data_ptr(),
+                                      outs[0].data_ptr(), None if k is None else outs[1].data_ptr(), handle),
+               "slra_qk_rope_fwd")
+    return tuple(outs)
+
+
+def qk_rope_bwd(prob: QkRope, q, k, dout_q, dout_k=None, wq=None, wk=None, positions=None, dq=None, dk=None,
+                workspace=None, stream=None):
+    """Gradients of sum(dout_q out_q) + sum(dout_k out_k) (slra_qk_rope_bwd): dq, dk in q's type, and the
+    weights' in fp32 where they are given.  dout_q, dout_k: q's type or fp32, any strides.  dq, dk may be
+    given (e.g. views of one fused gradient, or dout_q, dout_k themselves where the types agree).
+    workspace: as for residual_norm_bwd.  Returns QkRopeGrads, None where there is nothing."""
+    torch = _torch()
+    c = _qk_rope_problem(prob, wq, wk, positions, q.device)
+    c.x_dtype, c.out_dtype = _code(q), _code(dout_q)
+    if (k is not None) != (prob.kv_heads > 0) or (dout_k is not None) != (prob.kv_heads > 0):
+        raise ValueError(f"k, dout_k: the problem has {prob.kv_heads} key heads")
+    grads, weights = [], []
+    with _Call(q.device, stream) as handle:
+        for n, t, d, o, heads, w in (("q", q, dout_q, dq, prob.heads, wq), ("k", k, dout_k, dk, prob.kv_heads, wk)):
+            if t is None:
+                if o is not None:
+                    raise ValueError(f"d{n}: there is no {n}")
+                grads.append(None)
+                weights.append(None)
+                continue
+            shape = (prob.batch, prob.tokens, heads, prob.head_dim)
+            _expect(n, t, shape, q.dtype, q.device)
+            getattr(c, n + "_strides")[:] = _steps(t)
+            _expect("dout_" + n, d, shape, dout_q.dtype, q.device)
+            getattr(c, f"out_{n}_strides")[:] = _steps(d)
+            if o is None:
+                o = torch.empty(shape, dtype=q.dtype, device=q.device)
+            else:
+                _expect("d" + n, o, shape, q.dtype, q.device)
+                getattr(c, f"d{n}_strides")[:] = _steps(o)
+            grads.append(o)
+            weights.append(None if w is None else torch.empty(w.shape, dtype=torch.float32, device=q.device))
+            if w is not None:
+                setattr(c, f"dw{n}", weights[-1].data_ptr())
+        workspace = _sums_workspace("slra_qk_rope_bwd", c, workspace, q.device)
+        _check(lib().slra_qk_rope_bwd(ctypes.byref(c), q.data_ptr(), None if k is None else k.data_ptr(),
+                                      dout_q.data_ptr(), None if k is None else dout_k.data_ptr(), grads[0].data_ptr(),
+                                      None if k is None else grads[1].data_ptr(), workspace.data_ptr(),
+                                      workspace.numel(), handle), "slra_qk_rope_bwd")
+    return QkRopeGrads(grads[0], grads[1], weights[0], weights[1], workspace)

@@ -1,0 +1,215 @@
+"""Host-side checks of the operators around the attention (no GPU needed): defaults, validation of
+problems and arguments, workspace sizes.  Pointers are never dereferenced by the host."""
+import ctypes
+
+import pytest
+
+from sparse_rank_hybrid_b200 import build as B
+from sparse_rank_hybrid_b200 import slra
+
+BASE = 1 << 40  # made-up device addresses, 16 MiB apart
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import torch
+    B.build()
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses: on a machine without a GPU only")
+
+
+def at(i):
+    return BASE + (i << 24)
+
+
+def norm_problem(**kw):
+    c = slra._ResidualNorm()
+    assert slra.lib().slra_residual_norm_init(ctypes.byref(c), 2, 24, 64) == slra.OK
+    for n, v in kw.items():
+        if isinstance(v, tuple):
+            getattr(c, n)[:] = v
+        else:
+            setattr(c, n, v)
+    return c
+
+
+def norm_fwd(c, x=at(0), y=at(1), x_out=at(2), h=at(3)):
+    return slra.lib().slra_residual_norm_fwd(ctypes.byref(c), x, y, x_out, h, None)
+
+
+def norm_bwd(c, x=at(0), y=at(1), dx_out=at(2), dh=at(3), dx=at(4), dy=at(5), ws=at(6), n=1 << 24):
+    return slra.lib().slra_residual_norm_bwd(ctypes.byref(c), x, y, dx_out, dh, dx, dy, ws, n, None)
+
+
+def test_norm_defaults_reach_the_device_check():
+    c = norm_problem()
+    assert (c.groups, c.norm, c.post_norm, c.stream_dtype, c.mod_dtype) == (1, slra.NORM_LAYER, slra.NORM_NONE,
+                                                                             slra.DTYPE_BF16, slra.DTYPE_F32)
+    assert tuple(c.gate_strides) == (-1, -1) and c.residual_scale == 1.0
+    assert norm_fwd(c) == slra.ERR_NO_DEVICE and norm_bwd(c) == slra.ERR_NO_DEVICE
+    assert slra.lib().slra_residual_norm_init(None, 1, 1, 8) == slra.ERR_INVALID_ARG
+    assert norm_fwd(norm_problem(), y=None, x_out=None) == slra.ERR_NO_DEVICE
+    assert norm_fwd(norm_problem(norm=slra.NORM_NONE), h=None) == slra.ERR_NO_DEVICE
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(batch=0), slra.ERR_INVALID_ARG), (dict(tokens=0), slra.ERR_INVALID_ARG),
+    (dict(channels=0), slra.ERR_INVALID_ARG), (dict(groups=0), slra.ERR_INVALID_ARG),
+    (dict(groups=5), slra.ERR_INVALID_ARG), (dict(batch=1 << 16, tokens=1 << 16), slra.ERR_INVALID_ARG),
+    (dict(channels=60), slra.ERR_UNSUPPORTED), (dict(channels=8200), slra.ERR_UNSUPPORTED),
+    (dict(norm=3), slra.ERR_INVALID_ARG), (dict(post_norm=slra.NORM_LAYER), slra.ERR_INVALID_ARG),
+    (dict(stream_dtype=3), slra.ERR_INVALID_ARG), (dict(mod_dtype=-1), slra.ERR_INVALID_ARG),
+    (dict(block_dtype=slra.DTYPE_F16), slra.ERR_UNSUPPORTED),
+    (dict(stream_dtype=slra.DTYPE_F16, block_dtype=slra.DTYPE_F32), slra.ERR_UNSUPPORTED),
+    (dict(eps=0.0), slra.ERR_INVALID_ARG), (dict(eps=float("nan")), slra.ERR_INVALID_ARG),
+    (dict(post_eps=-1.0), slra.ERR_INVALID_ARG), (dict(residual_scale=float("inf")), slra.ERR_INVALID_ARG),
+    (dict(norm=slra.NORM_NONE, scale=at(8)), slra.ERR_INVALID_ARG),
+    (dict(norm=slra.NORM_RMS, bias=at(8)), slra.ERR_INVALID_ARG), (dict(post_weight=at(8)), slra.ERR_INVALID_ARG),
+    (dict(dgate=at(8)), slra.ERR_INVALID_ARG), (dict(dweight=at(8)), slra.ERR_INVALID_ARG),
+    (dict(scale=at(8) + 8), slra.ERR_ALIGNMENT), (dict(scale=at(8), dscale=at(9) + 4), slra.ERR_ALIGNMENT),
+    (dict(x_strides=(2048, 68)), slra.ERR_INVALID_ARG), (dict(x_strides=(2048, 0)), slra.ERR_INVALID_ARG),
+    (dict(scale=at(8), scale_strides=(-2, 0)), slra.ERR_INVALID_ARG),
+    (dict(scale=at(8), scale_strides=(2, 0)), slra.ERR_INVALID_ARG),
+    (dict(scale=at(8), scale_strides=(0, 0)), slra.ERR_NO_DEVICE),
+    (dict(x_strides=(4096, 72)), slra.ERR_NO_DEVICE),
+])
+def test_norm_problem_validation(kw, status):
+    c = norm_problem(**kw)
+    assert norm_bwd(c) == status
+    n = slra.lib().slra_residual_norm_bwd_workspace_bytes(ctypes.byref(c))
+    assert (n > 0) == (status == slra.ERR_NO_DEVICE)
+
+
+def test_norm_argument_validation():
+    INV, DEV = slra.ERR_INVALID_ARG, slra.ERR_NO_DEVICE
+    c = norm_problem()
+    assert norm_fwd(c, x=None) == INV and norm_fwd(c, h=None) == INV and norm_fwd(c, x_out=None) == INV
+    assert norm_fwd(c, y=None) == INV                        # x_out without y
+    assert norm_fwd(c, x=at(0) + 8) == slra.ERR_ALIGNMENT
+    assert norm_fwd(c, x_out=at(0)) == DEV and norm_fwd(c, h=at(1)) == DEV   # in place
+    assert norm_fwd(c, x_out=at(1)) == INV and norm_fwd(c, h=at(0)) == INV and norm_fwd(c, h=at(2)) == INV
+    assert norm_fwd(c, x_out=at(0) + 16) == INV
+    assert norm_fwd(norm_problem(scale=at(3) + 64)) == INV   # h over scale
+    assert norm_fwd(norm_problem(gate=at(8)), y=None, x_out=None) == INV
+    assert norm_fwd(norm_problem(residual_scale=0.5), y=None, x_out=None) == INV
+    assert norm_fwd(norm_problem(post_norm=slra.NORM_RMS), y=None, x_out=None) == INV
+    assert norm_fwd(norm_problem(norm=slra.NORM_NONE), y=None, x_out=None, h=None) == INV
+    assert norm_fwd(norm_problem(x_out_strides=(24 * 64, 32))) == INV  # output rows overlap
+    # two views of one buffer, rows interleaved: no overlap unless their columns do
+    i = dict(x_strides=(24 * 128, 128), x_out_strides=(24 * 128, 128))
+    assert norm_fwd(norm_problem(**i), x=at(0), x_out=at(0) + 128) == DEV
+    assert norm_fwd(norm_problem(**i), x=at(0), x_out=at(0) + 112) == INV
+    assert norm_bwd(c, dx_out=None) == DEV and norm_bwd(c, dh=None) == INV and norm_bwd(c, dx=None) == INV
+    assert norm_bwd(c, dx=at(2)) == DEV and norm_bwd(c, dy=at(3)) == DEV     # over dx_out, over dh
+    assert norm_bwd(c, dx=at(0)) == INV and norm_bwd(c, dy=at(4)) == INV and norm_bwd(c, dy=at(1)) == INV
+    assert norm_bwd(c, ws=at(0)) == INV
+    v = norm_problem(gate=at(8), dgate=at(9), scale=at(10), dscale=at(11), weight=at(12), dweight=at(13))
+    need = slra.lib().slra_residual_norm_bwd_workspace_bytes(ctypes.byref(v))
+    assert norm_bwd(v) == DEV and norm_bwd(v, ws=None, n=0) == DEV
+    assert norm_bwd(v, n=need - 1) == slra.ERR_WORKSPACE and norm_bwd(v, ws=at(6) + 16) == slra.ERR_WORKSPACE
+    v.dscale = at(9)
+    assert norm_bwd(v) == INV                                # two gradients in one place
+    v.dscale = at(10)
+    assert norm_bwd(v) == INV                                # a gradient over its vector
+
+
+def rope_problem(**kw):
+    c = slra._QkRope()
+    assert slra.lib().slra_qk_rope_init(ctypes.byref(c), 2, 24, 4, 64) == slra.OK
+    for n, v in dict(dict(kv_heads=2), **kw).items():
+        if isinstance(v, tuple):
+            getattr(c, n)[:] = v
+        else:
+            setattr(c, n, v)
+    return c
+
+
+def rope_fwd(c, q=at(0), k=at(1), oq=at(2), ok=at(3)):
+    return slra.lib().slra_qk_rope_fwd(ctypes.byref(c), q, k, oq, ok, None)
+
+
+def rope_bwd(c, q=at(0), k=at(1), gq=at(2), gk=at(3), dq=at(4), dk=at(5), ws=at(6), n=1 << 24):
+    return slra.lib().slra_qk_rope_bwd(ctypes.byref(c), q, k, gq, gk, dq, dk, ws, n, None)
+
+
+HEAD, TOKEN = slra.QK_NORM_HEAD, slra.QK_NORM_TOKEN
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), slra.ERR_NO_DEVICE), (dict(batch=0), slra.ERR_INVALID_ARG), (dict(heads=0), slra.ERR_INVALID_ARG),
+    (dict(kv_heads=-1), slra.ERR_INVALID_ARG), (dict(head_dim=60), slra.ERR_UNSUPPORTED),
+    (dict(head_dim=264), slra.ERR_UNSUPPORTED), (dict(heads=255, kv_heads=2), slra.ERR_UNSUPPORTED),
+    (dict(heads=1 << 40), slra.ERR_UNSUPPORTED),
+    (dict(batch=1 << 16, tokens=1 << 16), slra.ERR_INVALID_ARG), (dict(T=0), slra.ERR_INVALID_ARG),
+    (dict(W=23), slra.ERR_INVALID_ARG), (dict(first_token=1), slra.ERR_INVALID_ARG),
+    (dict(first_token=1, T=2), slra.ERR_NO_DEVICE), (dict(first_token=-1, T=2), slra.ERR_INVALID_ARG),
+    (dict(W=1, positions=at(8)), slra.ERR_NO_DEVICE), (dict(positions=at(8) + 2), slra.ERR_ALIGNMENT),
+    (dict(positions=at(8), positions_stride=71), slra.ERR_INVALID_ARG),
+    (dict(positions=at(8), positions_stride=72), slra.ERR_NO_DEVICE), (dict(W=0, rotate=0), slra.ERR_NO_DEVICE),
+    (dict(pos_offset=(0, (1 << 31) + 1, 0)), slra.ERR_INVALID_ARG), (dict(theta=float("nan")), slra.ERR_INVALID_ARG),
+    (dict(theta=-1.0), slra.ERR_INVALID_ARG), (dict(rope_split=(20, 10, 3)), slra.ERR_INVALID_ARG),
+    (dict(rope_split=(-1, 10, 3)), slra.ERR_INVALID_ARG), (dict(rope_split=(10, 10, 3)), slra.ERR_NO_DEVICE),
+    (dict(norm=3), slra.ERR_INVALID_ARG), (dict(rotate=2), slra.ERR_INVALID_ARG), (dict(pairing=2), slra.ERR_INVALID_ARG),
+    (dict(schedule=-1), slra.ERR_INVALID_ARG), (dict(x_dtype=3), slra.ERR_INVALID_ARG),
+    (dict(x_dtype=slra.DTYPE_F32), slra.ERR_UNSUPPORTED), (dict(out_dtype=slra.DTYPE_F16), slra.ERR_UNSUPPORTED),
+    (dict(out_dtype=slra.DTYPE_F32), slra.ERR_NO_DEVICE), (dict(eps=0.0, norm=HEAD), slra.ERR_INVALID_ARG),
+    (dict(wq=at(8)), slra.ERR_INVALID_ARG), (dict(norm=HEAD, wq=at(8)), slra.ERR_NO_DEVICE),
+    (dict(norm=HEAD, wq=at(8) + 8), slra.ERR_ALIGNMENT), (dict(norm=HEAD, dwq=at(8)), slra.ERR_INVALID_ARG),
+    (dict(norm=HEAD, wq=at(8), dwq=at(9), wk=at(10), dwk=at(11)), slra.ERR_NO_DEVICE),
+    (dict(norm=TOKEN, wq=at(8), dwq=at(9), wk=at(10), dwk=at(9)), slra.ERR_INVALID_ARG),
+    (dict(q_strides=(24 * 256, 256, 60)), slra.ERR_INVALID_ARG), (dict(q_strides=(24 * 512, 512, 64)), slra.ERR_NO_DEVICE),
+    (dict(dq_strides=(24 * 256, 256, 32)), slra.ERR_INVALID_ARG),  # rows of the gradient overlap
+])
+def test_rope_problem_validation(kw, status):
+    assert rope_bwd(rope_problem(**kw)) == status
+
+
+def test_rope_argument_validation():
+    INV, DEV = slra.ERR_INVALID_ARG, slra.ERR_NO_DEVICE
+    assert slra.lib().slra_qk_rope_init(None, 1, 1, 1, 64) == INV
+    c = rope_problem()
+    assert rope_fwd(c) == DEV and rope_fwd(c, q=None) == INV and rope_fwd(c, k=None) == INV and rope_fwd(c, ok=None) == INV
+    assert rope_fwd(rope_problem(kv_heads=0), k=None, ok=None) == DEV and rope_fwd(rope_problem(kv_heads=0)) == INV
+    assert rope_fwd(c, q=at(0) + 8) == slra.ERR_ALIGNMENT
+    assert rope_fwd(c, oq=at(0), ok=at(1)) == DEV and rope_fwd(c, oq=at(1)) == INV and rope_fwd(c, ok=at(2)) == INV
+    assert rope_fwd(c, oq=at(0) + 16) == INV
+    # fused [q | k | v] rows, in place
+    f = dict(zip(("q_strides", "k_strides", "out_q_strides", "out_k_strides"), [(24 * 512, 512, 64)] * 4))
+    assert rope_fwd(rope_problem(**f), at(0), at(0) + 512, at(0), at(0) + 512) == DEV
+    assert rope_fwd(rope_problem(**f), at(0), at(0) + 512, at(0) + 256, at(0) + 768) == INV
+    # q at another stride of heads over the same bytes is not in place
+    assert rope_fwd(rope_problem(heads=2, q_strides=(24 * 512, 512, 128), out_q_strides=(24 * 512, 512, 192)),
+                    oq=at(0)) == INV
+    # fp32 results over bf16 inputs are not in place
+    assert rope_fwd(rope_problem(out_dtype=slra.DTYPE_F32), oq=at(0)) == INV
+    assert rope_bwd(c, q=None, k=None) == DEV                # no norm: q and k are not read
+    h = rope_problem(norm=HEAD, wq=at(8), dwq=at(9))
+    assert rope_bwd(h) == DEV and rope_bwd(h, q=None) == INV and rope_bwd(h, k=None) == INV
+    assert rope_bwd(h, dq=at(2), dk=at(3)) == DEV and rope_bwd(h, dq=at(0)) == INV and rope_bwd(h, dq=at(9)) == INV
+    need = slra.lib().slra_qk_rope_bwd_workspace_bytes(ctypes.byref(h))
+    assert rope_bwd(h, n=need - 1) == slra.ERR_WORKSPACE and rope_bwd(h, ws=None, n=0) == DEV
+    assert rope_bwd(h, ws=at(0)) == INV and rope_bwd(rope_problem(positions=at(4) + 64, W=1)) == INV
+
+
+def test_workspaces_hold_a_bounded_number_of_partial_sums():
+    """The partial sums grow with the workers, which are bounded, not with the tokens."""
+    L = slra.lib()
+    sizes = []
+    for tokens in (1, 1000, 75600, 1 << 24):
+        c = norm_problem(batch=1, tokens=tokens, channels=5120, gate=at(8), dgate=at(9))
+        sizes.append(L.slra_residual_norm_bwd_workspace_bytes(ctypes.byref(c)))
+        r = rope_problem(batch=1, tokens=tokens, W=tokens, norm=TOKEN, wq=at(8), dwq=at(9), heads=40, kv_heads=40,
+                         head_dim=128)
+        assert 0 < L.slra_qk_rope_bwd_workspace_bytes(ctypes.byref(r)) < 1 << 26
+    assert sizes == sorted(sizes) and sizes[-1] == sizes[-2] < 1 << 26
+
+
+def test_binding_checks_its_tensors():
+    import torch
+    x = torch.zeros((1, 4, 64))
+    with pytest.raises(ValueError):
+        slra.residual_norm_fwd(slra.ResidualNorm(1, 4, 64), x)
+    with pytest.raises(ValueError):
+        slra.qk_rope_fwd(slra.QkRope(1, 4, 1, 64), x.view(1, 4, 1, 64))
+    with pytest.raises(ValueError):
+        slra.residual_norm_fwd(slra.ResidualNorm(1, 4, 64), x.double())
