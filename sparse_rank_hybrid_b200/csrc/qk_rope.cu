@@ -21,30 +21,28 @@
 namespace slra {
 namespace {
 
-constexpr int kMaxStages = 3;
-constexpr size_t kRingBytes = 200 * 1024;  // of a block's dynamic shared memory at most
+constexpr size_t kRingBytes = 200 * 1024;  // dynamic shared memory of an SM's blocks at most
 
 constexpr int rope_threads(int V) { return V == 1 ? 1024 : V == 2 ? 640 : 512; }
 
 // Eight elements of a head: consecutive ones (interleaved pairs), or four of the lower half and the four
 // they pair with in the upper half, `half` elements on.
 template <typename T, bool HALVES>
-__device__ __forceinline__ void copy_in(uint4* s, int step, const T* p, int half) {
+__device__ __forceinline__ void copy_in(const Ring& ring, int u, const T* p, int half) {
     if constexpr (!HALVES) {
-#pragma unroll
-        for (int i = 0; i < kUnits<T>; ++i) async_copy16(s + i * step, reinterpret_cast<const uint4*>(p) + i);
+        ring.copy(u, p);
     } else if constexpr (sizeof(T) == 4) {
-        async_copy16(s, p);
-        async_copy16(s + step, p + half);
+        async_copy16(ring.in + u * ring.unit, p);
+        async_copy16(ring.in + (u + 1) * ring.unit, p + half);
     } else {
-        async_copy8(s, p);
-        async_copy8(reinterpret_cast<uint2*>(s) + 1, p + half);
+        async_copy8(ring.in + u * ring.unit, p);
+        async_copy8(ring.in + u * ring.unit + 8, p + half);
     }
 }
 template <typename T, bool HALVES>
-__device__ __forceinline__ void store_out(T* p, int half, const float (&f)[8]) {
+__device__ __forceinline__ void store_out(T* p, int half, const Vec& v) {
     uint4 u[kUnits<T>];
-    pack8<T>(f, u);
+    pack<T>(v, u);
     if constexpr (!HALVES) {
 #pragma unroll
         for (int i = 0; i < kUnits<T>; ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
@@ -56,97 +54,114 @@ __device__ __forceinline__ void store_out(T* p, int half, const float (&f)[8]) {
         *reinterpret_cast<uint2*>(p + half) = make_uint2(u[0].z, u[0].w);
     }
 }
-template <bool HALVES>
-__device__ __forceinline__ float weight_at(const void* w, int dtype, int at, int half, int e) {
-    if (!w) return 1.f;
-    const int i = at + e + (HALVES && e >= 4 ? half - 4 : 0);
-    return dtype == kF32    ? static_cast<const float*>(w)[i]
-           : dtype == kBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i])
-                            : __half2float(static_cast<const __half*>(w)[i]);
+__device__ __forceinline__ float weight_at(const void* w, int dtype, int at) {
+    return dtype == kF32    ? static_cast<const float*>(w)[at]
+           : dtype == kBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[at])
+                            : __half2float(static_cast<const __half*>(w)[at]);
 }
 
+// The four pairs of a vector turned by their angles; the cos and sin of pairs (0, 1) and (2, 3) in c, s.
 template <bool HALVES>
-__device__ __forceinline__ void rotate(float (&f)[8], const float (&c)[4], const float (&s)[4], float sign) {
+__device__ __forceinline__ void rotate(Vec& v, const float2 (&c)[2], const float2 (&s)[2]) {
+    if constexpr (HALVES) {  // pairs m and m + 4: two pairs at once
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-        const int i = HALVES ? m : 2 * m, j = HALVES ? m + 4 : 2 * m + 1;
-        const float a = f[i], b = f[j], sn = sign * s[m];
-        f[i] = a * c[m] - b * sn;
-        f[j] = a * sn + b * c[m];
+        for (int m = 0; m < 2; ++m) {
+            const float2 lo = v.f[m], hi = v.f[m + 2], neg = make_float2(-s[m].x, -s[m].y);
+            v.f[m] = fma2(hi, neg, mul2(lo, c[m]));
+            v.f[m + 2] = fma2(hi, c[m], mul2(lo, s[m]));
+        }
+    } else {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const float cc = m & 1 ? c[m / 2].y : c[m / 2].x, ss = m & 1 ? s[m / 2].y : s[m / 2].x;
+            const float2 p = v.f[m];
+            v.f[m] = make_float2(fmaf(-p.y, ss, p.x * cc), fmaf(p.y, cc, p.x * ss));
+        }
     }
 }
 
-template <typename TX, typename TO, int V, bool HALVES, bool BWD>
-__global__ void __launch_bounds__(rope_threads(V)) qk_rope_kernel(const __grid_constant__ QkRopeArgs a) {
-    constexpr int UX = kUnits<TX>, UD = BWD ? kUnits<TO> : 0, U = V * (UX + UD);
+template <typename TX, typename TO, int V, bool HALVES, bool BWD, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? rope_threads(V) : 128) qk_rope_kernel(const __grid_constant__ QkRopeArgs a) {
+    constexpr int UX = kUnits<TX>, UD = BWD ? kUnits<TO> : 0, ONE = UX + UD, U = V * ONE;
     using TW = typename std::conditional<BWD, TX, TO>::type;  // type of what is written
-    extern __shared__ uint4 ring[];
-    __shared__ float scratch[kTeamScratch];
+    extern __shared__ uint4 shared[];
+    __shared__ __align__(16) float scratch[kTeamScratch];
     __shared__ double turns[kRopeMaxPairs];
     __shared__ int axis[kRopeMaxPairs];
     const int D = a.head_dim, pairs = D / 2, half = HALVES ? D / 2 : 0, G = a.group;
-    const int t = threadIdx.x % a.team, lane = t % G, in_block = threadIdx.x / a.team;
-    const int teams = blockDim.x / a.team, worker = blockIdx.x * teams + in_block;
-    const int heads = a.side[0].heads + a.side[1].heads;
-    Team team{a.team, scratch, 0};
-    // cos and sin of the current and the next token: [2][2][pairs] floats a team, behind the ring
-    float* table = reinterpret_cast<float*>(ring + static_cast<size_t>(a.stages) * U * blockDim.x) + in_block * 4 * pairs;
+    const int team_size = WIDE ? blockDim.x : a.team;
+    const int t = WIDE ? threadIdx.x : threadIdx.x % a.team, lane = t % G;
+    const int in_block = WIDE ? 0 : threadIdx.x / a.team, teams = WIDE ? 1 : blockDim.x / a.team;
+    const int worker = blockIdx.x * teams + in_block;
+    const int q_heads = a.side[0].heads, heads = q_heads + a.side[1].heads;
     for (int j = threadIdx.x; j < pairs; j += blockDim.x) turns[j] = a.turns[j], axis[j] = a.axis[j];
+    Team<WIDE> team(team_size, scratch);
     __syncthreads();
+    // cos and sin of the current and the next token: [2][2][pairs] floats a team, behind the ring
+    float* table = reinterpret_cast<float*>(shared + static_cast<size_t>(a.stages) * U * blockDim.x) + in_block * 4 * pairs;
 
     const long long r0 = worker_lo(a.rows, a.workers, worker), r1 = worker_lo(a.rows, a.workers, worker + 1);
     const int n = static_cast<int>(r1 - r0);
-    const int iters = a.team <= 32 ? static_cast<int>((a.rows + a.workers - 1) / a.workers) : n;
+    const int iters = WIDE ? n : static_cast<int>((a.rows + a.workers - 1) / a.workers);
     const int b0 = static_cast<int>(r0 / a.tokens), l0 = static_cast<int>(r0 % a.tokens);
     const bool need_x = !BWD || a.norm != kQkNormNone;
 
     // this thread's vectors: which side and head, where, and whether there is one
+    Ring ring(shared_address(shared), a.stages, U);
     const TX* px[V];
     const TO* pd[V];
     TW* po[V];
-    float w[V][8], dw[V][8];
-    bool is_k[V], live[V];
+    Vec w[V], dw[V];
+    bool is_k[V], on[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int head = (t + v * a.team) / G;
-        live[v] = head < heads && lane * 8 < D;
-        is_k[v] = head >= a.side[0].heads;
+        const int head = (t + v * team_size) / G;
+        on[v] = head < heads && lane * 8 < D;
+        is_k[v] = head >= q_heads;
         const RopeSide& s = a.side[is_k[v]];
-        const int h = live[v] ? head - (is_k[v] ? a.side[0].heads : 0) : 0, c = lane * (HALVES ? 4 : 8);
+        const int h = on[v] ? head - (is_k[v] ? q_heads : 0) : 0, c = lane * (HALVES ? 4 : 8);
         px[v] = static_cast<const TX*>(s.x) + s.sx.row(b0, l0, h) + c;
         pd[v] = static_cast<const TO*>(s.d) + s.sd.row(b0, l0, h) + c;
         po[v] = static_cast<TW*>(s.out) + s.so.row(b0, l0, h) + c;
+        if (!on[v]) ring.clear(v * ONE, ONE);
+        w[v] = vec_of(1.f);
+        dw[v] = vec_of(0.f);
+        if (on[v] && a.norm && s.weight) {
+            const int at = (a.norm == kQkNormToken ? h * D : 0) + c, up = at + (HALVES ? half : 4);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            w[v][e] = live[v] && a.norm ? weight_at<HALVES>(s.weight, a.w_dtype, (a.norm == kQkNormToken ? h * D : 0) + c, half, e) : 1.f;
-            dw[v][e] = 0.f;
+            for (int e = 0; e < 2; ++e) {
+                w[v].f[e] = make_float2(weight_at(s.weight, a.w_dtype, at + 2 * e), weight_at(s.weight, a.w_dtype, at + 2 * e + 1));
+                w[v].f[e + 2] = make_float2(weight_at(s.weight, a.w_dtype, up + 2 * e), weight_at(s.weight, a.w_dtype, up + 2 * e + 1));
+            }
         }
     }
 
     int lp = l0, left = n;
-    auto prefetch = [&](int stage) {
+    auto prefetch = [&]() {
         if (left > 0) {
             --left;
-            uint4* s = ring + static_cast<size_t>(stage) * U * blockDim.x + threadIdx.x;
             const bool last = ++lp == a.tokens;
             if (last) lp = 0;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                if (!live[v]) continue;
-                const RopeSide& side = a.side[is_k[v]];
+                const RopeSide& q = a.side[0];
+                const RopeSide& k = a.side[1];
                 if (need_x) {
-                    copy_in<TX, HALVES>(s + v * UX * blockDim.x, blockDim.x, px[v], half);
-                    px[v] += last ? side.sx.b - (a.tokens - 1) * side.sx.l : side.sx.l;
+                    if (on[v]) copy_in<TX, HALVES>(ring, v * ONE, px[v], half);
+                    px[v] += is_k[v] ? k.sx.l : q.sx.l;
+                    if (last) px[v] += is_k[v] ? k.sx.b - a.tokens * k.sx.l : q.sx.b - a.tokens * q.sx.l;
                 }
                 if (BWD) {
-                    copy_in<TO, HALVES>(s + (V * UX + v * UD) * blockDim.x, blockDim.x, pd[v], half);
-                    pd[v] += last ? side.sd.b - (a.tokens - 1) * side.sd.l : side.sd.l;
+                    if (on[v]) copy_in<TO, HALVES>(ring, v * ONE + UX, pd[v], half);
+                    pd[v] += is_k[v] ? k.sd.l : q.sd.l;
+                    if (last) pd[v] += is_k[v] ? k.sd.b - a.tokens * k.sd.l : q.sd.b - a.tokens * q.sd.l;
                 }
             }
+            ring.filled();
         }
         async_commit();
     };
-    for (int s = 0; s < a.stages - 1; ++s) prefetch(s);
+    for (int s = 0; s < a.stages - 1; ++s) prefetch();
 
     // The table of the row whose batch and token are (tb, tl), in half `which` of the team's table; its
     // grid place (gt, gh, gw) moves along with it.
@@ -156,14 +171,14 @@ __global__ void __launch_bounds__(rope_threads(V)) qk_rope_kernel(const __grid_c
     if (!a.positions && a.rotate) gh = static_cast<int>(start % hw) / a.W, gw = static_cast<int>(start % hw) % a.W;
     auto fill = [&](int which) {
         float* cs = table + which * 2 * pairs;
-        for (int j = t; j < pairs; j += a.team) {
+        for (int j = t; j < pairs; j += team_size) {
             const int ax = axis[j];
             const int p = a.positions ? a.positions[tb * a.positions_b + tl * 3ll + ax] : ax == 0 ? gt : ax == 1 ? gh : gw;
             const double turn = static_cast<double>(p + a.offset[ax]) * turns[j];
             float sn, c;
             sincospif(2.0f * static_cast<float>(turn - rint(turn)), &sn, &c);
             cs[j] = c;
-            cs[pairs + j] = sn;
+            cs[pairs + j] = BWD ? -sn : sn;  // the gradient turns back
         }
         if (++tl == a.tokens) {
             tl = 0, ++tb;
@@ -179,123 +194,107 @@ __global__ void __launch_bounds__(rope_threads(V)) qk_rope_kernel(const __grid_c
     }
 
     const float inv_head = 1.0f / D;
-    const float inv_q = 1.0f / (static_cast<float>(D) * a.side[0].heads);
+    const float inv_q = 1.0f / (static_cast<float>(D) * q_heads);
     const float inv_k = 1.0f / (static_cast<float>(D) * max(1, a.side[1].heads));
-    int stage = 0, l = l0;
+    const bool has_pairs = lane * 8 < D;
+    int l = l0;
     for (int i = 0; i < iters; ++i) {
-        prefetch(stage == 0 ? a.stages - 1 : stage - 1);
-        const bool row = i < n;
-        float c[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+        prefetch();
+        const bool row = WIDE || i < n;
+        float2 c[2] = {both(1.f), both(1.f)}, sn[2] = {both(0.f), both(0.f)};
         if (a.rotate) {
-            if (row && lane * 8 < D) {
+            if (has_pairs) {
                 const float4* cs = reinterpret_cast<const float4*>(table + (i & 1) * 2 * pairs);
                 const float4 u = cs[lane], z = cs[pairs / 4 + lane];
-                c[0] = u.x, c[1] = u.y, c[2] = u.z, c[3] = u.w;
-                sn[0] = z.x, sn[1] = z.y, sn[2] = z.z, sn[3] = z.w;
+                c[0] = make_float2(u.x, u.y), c[1] = make_float2(u.z, u.w);
+                sn[0] = make_float2(z.x, z.y), sn[1] = make_float2(z.z, z.w);
             }
             if (i + 1 < n) fill((i + 1) & 1);
             // every thread has read this row's table and sees the next one after a barrier of the team
-            if (a.norm != kQkNormToken || a.team <= 32) team.sync();
+            if (!WIDE || a.norm != kQkNormToken) team.sync();
         }
-        if (a.stages == 3) async_wait<2>();
-        else if (a.stages == 2) async_wait<1>();
-        else async_wait<0>();
-        const uint4* s = ring + static_cast<size_t>(stage) * U * blockDim.x + threadIdx.x;
-        if (++stage == a.stages) stage = 0;
+        ring_wait(a.stages);
 
-        float x[V][8], g[V][8];
+        Vec x[V], g[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const bool on = row && live[v];
-            if (on && need_x) {
-                uint4 u[UX];
-#pragma unroll
-                for (int k = 0; k < UX; ++k) u[k] = s[(v * UX + k) * blockDim.x];
-                unpack8<TX>(u, x[v]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[v][e] = 0.f;
-            }
+            if (need_x) x[v] = ring.read<TX>(v * ONE);
             if (BWD) {
-                if (on) {
-                    uint4 u[kUnits<TO>];
-#pragma unroll
-                    for (int k = 0; k < UD; ++k) u[k] = s[(V * UX + v * UD + k) * blockDim.x];
-                    unpack8<TO>(u, g[v]);
-                    rotate<HALVES>(g[v], c, sn, -1.f);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) g[v][e] = 0.f;
-                }
+                g[v] = ring.read<TO>(v * ONE + UX);
+                if (a.rotate) rotate<HALVES>(g[v], c, sn);
             }
         }
+        ring.done();
         // per vector: r, and r^2 mean(g w x) of the norm it belongs to
         float r[V], gx[V];
-        if (a.norm == kQkNormHead) {
+        if (a.norm) {
+            float qq[V], z[V];
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                float q = 0.f, z = 0.f;
+                float2 s1 = mul2(x[v].f[0], x[v].f[0]), s2 = both(0.f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    q += x[v][e] * x[v][e];
-                    if (BWD) z += g[v][e] * w[v][e] * x[v][e];
-                }
-                for (int o = G >> 1; o > 0; o >>= 1) {
-                    q += __shfl_xor_sync(0xffffffffu, q, o);
-                    if (BWD) z += __shfl_xor_sync(0xffffffffu, z, o);
-                }
-                r[v] = rsqrtf(q * inv_head + a.eps);
-                gx[v] = z * inv_head * r[v] * r[v];
+                for (int e = 1; e < 4; ++e) s1 = fma2(x[v].f[e], x[v].f[e], s1);
+                if (BWD)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s2 = fma2(mul2(g[v].f[e], w[v].f[e]), x[v].f[e], s2);
+                qq[v] = fold(s1);
+                z[v] = BWD ? fold(s2) : 0.f;
             }
-        } else if (a.norm == kQkNormToken) {
-            float q[BWD ? 4 : 2] = {};
+            if (a.norm == kQkNormHead) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float qq = 0.f, z = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    qq += x[v][e] * x[v][e];
-                    if (BWD) z += g[v][e] * w[v][e] * x[v][e];
+                for (int v = 0; v < V; ++v) {
+                    for (int o = G >> 1; o > 0; o >>= 1) {
+                        qq[v] += Team<WIDE>::swap(qq[v], o);
+                        if (BWD) z[v] += Team<WIDE>::swap(z[v], o);
+                    }
+                    r[v] = rsqrtf(qq[v] * inv_head + a.eps);
+                    if (BWD) gx[v] = z[v] * inv_head * r[v] * r[v];
                 }
-                q[0] += is_k[v] ? 0.f : qq;
-                q[1] += is_k[v] ? qq : 0.f;
-                if (BWD) {
-                    q[BWD ? 2 : 0] += is_k[v] ? 0.f : z;
-                    q[BWD ? 3 : 0] += is_k[v] ? z : 0.f;
-                }
-            }
-            team.sum(q);
-            const float rq = rsqrtf(q[0] * inv_q + a.eps), rk = rsqrtf(q[1] * inv_k + a.eps);
+            } else {
+                float q[BWD ? 4 : 2] = {};
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                r[v] = is_k[v] ? rk : rq;
-                if (BWD) gx[v] = is_k[v] ? q[BWD ? 3 : 0] * inv_k * rk * rk : q[BWD ? 2 : 0] * inv_q * rq * rq;
+                for (int v = 0; v < V; ++v) {
+                    q[0] += is_k[v] ? 0.f : qq[v];
+                    q[1] += is_k[v] ? qq[v] : 0.f;
+                    if constexpr (BWD) {
+                        q[2] += is_k[v] ? 0.f : z[v];
+                        q[3] += is_k[v] ? z[v] : 0.f;
+                    }
+                }
+                team.sum(q);
+                const float rq = rsqrtf(q[0] * inv_q + a.eps), rk = rsqrtf(q[1] * inv_k + a.eps);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    r[v] = is_k[v] ? rk : rq;
+                    if constexpr (BWD) gx[v] = is_k[v] ? q[3] * inv_k * rk * rk : q[2] * inv_q * rq * rq;
+                }
             }
         }
-        if (row) {
-            const bool last = ++l == a.tokens;
-            if (last) l = 0;
+        const bool last = l + 1 == a.tokens;
+        l = last ? 0 : l + 1;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (!live[v]) continue;
-                const RopeSide& side = a.side[is_k[v]];
-                if (!BWD) {
-                    if (a.norm)
+        for (int v = 0; v < V; ++v) {
+            if (!BWD) {
+                if (a.norm)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) x[v][e] = x[v][e] * r[v] * w[v][e];
-                    rotate<HALVES>(x[v], c, sn, 1.f);
-                    store_out<TW, HALVES>(po[v], half, x[v]);
-                } else {
-                    if (a.norm)
+                    for (int e = 0; e < 4; ++e) x[v].f[e] = mul2(x[v].f[e], mul2(w[v].f[e], both(r[v])));
+                if (a.rotate) rotate<HALVES>(x[v], c, sn);
+                if (row && on[v]) store_out<TW, HALVES>(po[v], half, x[v]);
+            } else {
+                if (a.norm) {
+                    const float2 rr = both(r[v]), mg = both(-gx[v]);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            dw[v][e] = fmaf(g[v][e], x[v][e] * r[v], dw[v][e]);
-                            g[v][e] = r[v] * (g[v][e] * w[v][e] - x[v][e] * gx[v]);
-                        }
-                    store_out<TW, HALVES>(po[v], half, g[v]);
+                    for (int e = 0; e < 4; ++e) {
+                        if (row) dw[v].f[e] = fma2(g[v].f[e], mul2(x[v].f[e], rr), dw[v].f[e]);
+                        g[v].f[e] = mul2(rr, fma2(x[v].f[e], mg, mul2(g[v].f[e], w[v].f[e])));
+                    }
                 }
-                po[v] += last ? side.so.b - (a.tokens - 1) * side.so.l : side.so.l;
+                if (row && on[v]) store_out<TW, HALVES>(po[v], half, g[v]);
             }
+            const Strides& sq = a.side[0].so;
+            const Strides& sk = a.side[1].so;
+            po[v] += is_k[v] ? sk.l : sq.l;
+            if (last) po[v] += is_k[v] ? sk.b - a.tokens * sk.l : sq.b - a.tokens * sq.l;
         }
     }
 
@@ -304,33 +303,26 @@ __global__ void __launch_bounds__(rope_threads(V)) qk_rope_kernel(const __grid_c
         float* part = a.part + static_cast<long long>(worker) * heads * D;
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (live[v]) store_out<float, HALVES>(part + (t + v * a.team) / G * D + lane * (HALVES ? 4 : 8), half, dw[v]);
+            if (on[v]) store_out<float, HALVES>(part + (t + v * team_size) / G * D + lane * (HALVES ? 4 : 8), half, dw[v]);
         return;
     }
     // one weight for all heads of a side: joined over the heads in order, through the ring's memory
     async_wait<0>();
     __syncthreads();
-    float4* sums = reinterpret_cast<float4*>(ring);
+    Vec* sums = reinterpret_cast<Vec*>(shared);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            sums[(v * 2 + k) * blockDim.x + threadIdx.x] =
-                make_float4(dw[v][4 * k], dw[v][4 * k + 1], dw[v][4 * k + 2], dw[v][4 * k + 3]);
+    for (int v = 0; v < V; ++v) sums[v * blockDim.x + threadIdx.x] = dw[v];
     __syncthreads();
-    const int sides = a.side[1].heads > 0 ? 2 : 1;
-    for (int j = t; j < sides * G; j += a.team) {
+    const int sides = heads > q_heads ? 2 : 1;
+    for (int j = t; j < sides * G; j += team_size) {
         const int side = j / G, place = j % G;
         if (place * 8 >= D) continue;
-        const int h0 = side ? a.side[0].heads : 0, h1 = side ? heads : a.side[0].heads;
-        float d[8] = {};
-        for (int h = h0; h < h1; ++h) {
-            const int slot = h * G + place, v = slot / a.team, at = in_block * a.team + slot % a.team;
+        Vec d = vec_of(0.f);
+        for (int h = side ? q_heads : 0; h < (side ? heads : q_heads); ++h) {
+            const int slot = h * G + place, v = slot / team_size, at = in_block * team_size + slot % team_size;
+            const Vec u = sums[v * blockDim.x + at];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float4 u = sums[(v * 2 + k) * blockDim.x + at];
-                d[4 * k] += u.x, d[4 * k + 1] += u.y, d[4 * k + 2] += u.z, d[4 * k + 3] += u.w;
-            }
+            for (int e = 0; e < 4; ++e) d.f[e] = add2(d.f[e], u.f[e]);
         }
         store_out<float, HALVES>(a.part + (static_cast<long long>(worker) * sides + side) * D + place * (HALVES ? 4 : 8),
                                  half, d);
@@ -364,13 +356,16 @@ int group_of(int head_dim) {
     return g;
 }
 
-template <typename TX, typename TO, int V, bool HALVES, bool BWD>
+// Blocks that a processor holds at once, from the registers the kernels need.
+int blocks_per_sm(const RowPlan& p, bool backward) { return std::max(1, (p.V == 1 ? 1024 : 640) / p.threads); }
+
+template <typename TX, typename TO, int V, bool HALVES, bool BWD, bool WIDE>
 cudaError_t launch(QkRopeArgs a, const RowPlan& p, cudaStream_t st) {
     const size_t stage = size_t(16) * V * (kUnits<TX> + (BWD ? kUnits<TO> : 0)) * p.threads;
-    a.stages = kMaxStages;
-    while (a.stages > 1 && a.stages * stage > kRingBytes) --a.stages;
+    const int per_sm = blocks_per_sm(p, BWD);
+    a.stages = ring_stages(stage, per_sm, kRingBytes / per_sm);
     const size_t smem = a.stages * stage + size_t(p.threads / p.team) * 2 * a.head_dim * sizeof(float);
-    const auto kernel = qk_rope_kernel<TX, TO, V, HALVES, BWD>;
+    const auto kernel = qk_rope_kernel<TX, TO, V, HALVES, BWD, WIDE>;
     if (smem > 40 * 1024) {  // 48 KB without opting in, less the static part
         const cudaError_t e =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -379,38 +374,29 @@ cudaError_t launch(QkRopeArgs a, const RowPlan& p, cudaStream_t st) {
     kernel<<<p.blocks, p.threads, smem, st>>>(a);
     return cudaGetLastError();
 }
-template <typename TX, typename TO, int V>
+template <typename TX, typename TO, int V, bool WIDE>
 cudaError_t launch_dir(const QkRopeArgs& a, const RowPlan& p, bool backward, cudaStream_t st) {
     if (a.halves)
-        return backward ? launch<TX, TO, V, true, true>(a, p, st) : launch<TX, TO, V, true, false>(a, p, st);
-    return backward ? launch<TX, TO, V, false, true>(a, p, st) : launch<TX, TO, V, false, false>(a, p, st);
+        return backward ? launch<TX, TO, V, true, true, WIDE>(a, p, st) : launch<TX, TO, V, true, false, WIDE>(a, p, st);
+    return backward ? launch<TX, TO, V, false, true, WIDE>(a, p, st) : launch<TX, TO, V, false, false, WIDE>(a, p, st);
 }
 template <typename TX, typename TO>
 cudaError_t launch_types(const QkRopeArgs& a, const RowPlan& p, bool backward, cudaStream_t st) {
-    return p.V == 1   ? launch_dir<TX, TO, 1>(a, p, backward, st)
-           : p.V == 2 ? launch_dir<TX, TO, 2>(a, p, backward, st)
-                      : launch_dir<TX, TO, 4>(a, p, backward, st);
+    return p.team <= 32 ? launch_dir<TX, TO, 1, false>(a, p, backward, st)
+           : p.V == 1   ? launch_dir<TX, TO, 1, true>(a, p, backward, st)
+           : p.V == 2   ? launch_dir<TX, TO, 2, true>(a, p, backward, st)
+                        : launch_dir<TX, TO, 4, true>(a, p, backward, st);
 }
 
 }  // namespace
 
 RowPlan qk_rope_plan(long long rows, int head_dim, int heads, bool backward) {
     RowPlan p;
-    const int G = group_of(head_dim), slots = heads * G;
-    p.V = 1;
-    if (slots <= 32) {
-        p.team = 1;
-        while (p.team < slots) p.team *= 2;
-        p.threads = 128;
-    } else {
-        while (p.V < 4 && (slots + p.V - 1) / p.V > rope_threads(p.V)) p.V *= 2;
-        p.team = p.threads = ((slots + p.V - 1) / p.V + 31) / 32 * 32;
-    }
-    const int teams = p.threads / p.team;
-    const int per_sm = std::max(1, (backward ? 640 : 1024) / p.threads);
-    const long long want = (rows + teams - 1) / teams;
-    p.blocks = static_cast<int>(std::min<long long>(want, std::min(kSMs * per_sm, kMaxWorkers / teams)));
-    p.workers = p.blocks * teams;
+    const int slots = heads * group_of(head_dim);
+    int V = 1;
+    while (V < 4 && (slots + V - 1) / V > rope_threads(V)) V *= 2;
+    row_team(slots, V, &p);
+    row_workers(rows, kSMs * blocks_per_sm(p, backward), &p);
     return p;
 }
 

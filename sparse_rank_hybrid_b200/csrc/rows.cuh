@@ -1,5 +1,10 @@
 // Helpers of the row kernels (residual_norm.cu, qk_rope.cu): typed vectors of eight elements, each
 // thread's own ring of asynchronous loads, and sums over the threads that share a row.
+//
+// These kernels move few bytes per element and are bound by memory only while they issue few enough
+// instructions: an SM has about 22 bytes of HBM bandwidth a clock, so a vector of eight bf16 elements read
+// and written leaves its warp some 180 issue slots.  Hence the packed fp32 arithmetic (two lanes of a
+// register pair an instruction) and the sums that halve the values they carry at each exchange.
 #pragma once
 
 #include "common.cuh"
@@ -9,159 +14,269 @@ namespace slra {
 // Element types of the tensors, as the values of slra_dtype.
 constexpr int kBf16 = 0, kF32 = 1, kF16 = 2;
 
-// Eight elements of a tensor: one 16-byte unit of a 16-bit type, two of fp32.
+// Packed fp32 arithmetic: two independent IEEE operations.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(d)
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
+    return reinterpret_cast<float2&>(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return reinterpret_cast<float2&>(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return reinterpret_cast<float2&>(d);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float fold(float2 a) { return a.x + a.y; }
+
+// Eight elements of a row, in fp32.
+struct Vec {
+    float2 f[4];
+};
+__device__ __forceinline__ Vec vec_of(float x) {
+    Vec v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v.f[i] = both(x);
+    return v;
+}
+
+// In memory: one 16-byte unit of a 16-bit type, two of fp32.
 template <typename T>
 constexpr int kUnits = sizeof(T) / 2;
 
 template <typename T>
-__device__ __forceinline__ void unpack8(const uint4 (&u)[kUnits<T>], float (&f)[8]);
+__device__ __forceinline__ Vec unpack(const uint4 (&u)[kUnits<T>]);
 template <>
-__device__ __forceinline__ void unpack8<__nv_bfloat16>(const uint4 (&u)[1], float (&f)[8]) {
+__device__ __forceinline__ Vec unpack<__nv_bfloat16>(const uint4 (&u)[1]) {
     const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+    Vec v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {  // bf16 is the upper half of fp32
-        f[2 * i] = __uint_as_float(w[i] << 16);
-        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i)  // bf16 is the upper half of fp32
+        v.f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    return v;
 }
 template <>
-__device__ __forceinline__ void unpack8<__half>(const uint4 (&u)[1], float (&f)[8]) {
+__device__ __forceinline__ Vec unpack<__half>(const uint4 (&u)[1]) {
     const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+    Vec v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2 h = *reinterpret_cast<const __half2*>(&w[i]);
-        f[2 * i] = __low2float(h);
-        f[2 * i + 1] = __high2float(h);
-    }
+    for (int i = 0; i < 4; ++i) v.f[i] = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    return v;
 }
 template <>
-__device__ __forceinline__ void unpack8<float>(const uint4 (&u)[2], float (&f)[8]) {
+__device__ __forceinline__ Vec unpack<float>(const uint4 (&u)[2]) {
+    Vec v;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        f[4 * i] = __uint_as_float(u[i].x);
-        f[4 * i + 1] = __uint_as_float(u[i].y);
-        f[4 * i + 2] = __uint_as_float(u[i].z);
-        f[4 * i + 3] = __uint_as_float(u[i].w);
+        v.f[2 * i] = make_float2(__uint_as_float(u[i].x), __uint_as_float(u[i].y));
+        v.f[2 * i + 1] = make_float2(__uint_as_float(u[i].z), __uint_as_float(u[i].w));
     }
+    return v;
 }
 
 // Rounded to nearest even, once, on the way to memory.
 template <typename T>
-__device__ __forceinline__ void pack8(const float (&f)[8], uint4 (&u)[kUnits<T>]);
+__device__ __forceinline__ void pack(const Vec& v, uint4 (&u)[kUnits<T>]);
 template <>
-__device__ __forceinline__ void pack8<__nv_bfloat16>(const float (&f)[8], uint4 (&u)[1]) {
+__device__ __forceinline__ void pack<__nv_bfloat16>(const Vec& v, uint4 (&u)[1]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v.f[i].x, v.f[i].y);
         w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
     u[0] = make_uint4(w[0], w[1], w[2], w[3]);
 }
 template <>
-__device__ __forceinline__ void pack8<__half>(const float (&f)[8], uint4 (&u)[1]) {
+__device__ __forceinline__ void pack<__half>(const Vec& v, uint4 (&u)[1]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        const __half2 h = __floats2half2_rn(v.f[i].x, v.f[i].y);
         w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
     u[0] = make_uint4(w[0], w[1], w[2], w[3]);
 }
 template <>
-__device__ __forceinline__ void pack8<float>(const float (&f)[8], uint4 (&u)[2]) {
+__device__ __forceinline__ void pack<float>(const Vec& v, uint4 (&u)[2]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-        u[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
-                          __float_as_uint(f[4 * i + 3]));
+        u[i] = make_uint4(__float_as_uint(v.f[2 * i].x), __float_as_uint(v.f[2 * i].y),
+                          __float_as_uint(v.f[2 * i + 1].x), __float_as_uint(v.f[2 * i + 1].y));
 }
 
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
+__device__ __forceinline__ Vec load_vec(const T* p) {
     uint4 u[kUnits<T>];
 #pragma unroll
     for (int i = 0; i < kUnits<T>; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-    unpack8<T>(u, f);
+    return unpack<T>(u);
 }
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
+__device__ __forceinline__ void store_vec(T* p, const Vec& v) {
     uint4 u[kUnits<T>];
-    pack8<T>(f, u);
+    pack<T>(v, u);
 #pragma unroll
     for (int i = 0; i < kUnits<T>; ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
 }
 
 // Eight elements of a vector whose type is known at run time (weights, modulation rows), or `fill`
 // where there is no such vector.
-__device__ __forceinline__ void load8_any(const void* base, long long at, int dtype, float fill, float (&f)[8]) {
-    if (!base) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = fill;
-    } else if (dtype == kF32) {
-        load8(static_cast<const float*>(base) + at, f);
-    } else if (dtype == kBf16) {
-        load8(static_cast<const __nv_bfloat16*>(base) + at, f);
-    } else {
-        load8(static_cast<const __half*>(base) + at, f);
-    }
+__device__ __forceinline__ Vec load_any(const void* base, long long at, int dtype, float fill) {
+    if (!base) return vec_of(fill);
+    if (dtype == kF32) return load_vec(static_cast<const float*>(base) + at);
+    if (dtype == kBf16) return load_vec(static_cast<const __nv_bfloat16*>(base) + at);
+    return load_vec(static_cast<const __half*>(base) + at);
 }
 
 // Asynchronous copies global -> shared.  Every thread reads back only what it copied itself, so its own
 // wait orders the data and no barrier is needed.
-__device__ __forceinline__ void async_copy16(void* smem, const void* gmem) {
-    const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s), "l"(gmem) : "memory");
+__device__ __forceinline__ void async_copy16(uint32_t smem, const void* gmem) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem) : "memory");
 }
-__device__ __forceinline__ void async_copy8(void* smem, const void* gmem) {
-    const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(s), "l"(gmem) : "memory");
+__device__ __forceinline__ void async_copy8(uint32_t smem, const void* gmem) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem), "l"(gmem) : "memory");
 }
 __device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ uint4 shared16(uint32_t smem) {
+    uint4 u;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                 : "r"(smem)
+                 : "memory");
+    return u;
+}
+__device__ __forceinline__ uint32_t shared_address(const void* p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
 
-// A team of threads shares a row: `size` threads, a power of two up to 32 (several teams in a block) or
-// the whole block of `size` = blockDim.x threads, a multiple of 32.
+// A thread's own part of a ring of `stages` rows: unit u of the stage at `at` is at + u * unit.  One stage
+// is filled (at `in`) while the oldest is read (at `out`).
+struct Ring {
+    uint32_t in, out, first, last, stage, unit;
+    // `units` 16-byte units a thread and stage
+    __device__ Ring(uint32_t base, int stages, int units) {
+        unit = blockDim.x * 16;
+        stage = unit * units;
+        first = in = out = base + threadIdx.x * 16;
+        last = first + stage * (stages - 1);
+    }
+    __device__ __forceinline__ void filled() { in = in == last ? first : in + stage; }
+    __device__ __forceinline__ void done() { out = out == last ? first : out + stage; }
+    template <typename T>
+    __device__ __forceinline__ void copy(int u, const T* p) const {
+#pragma unroll
+        for (int i = 0; i < kUnits<T>; ++i) async_copy16(in + (u + i) * unit, reinterpret_cast<const uint4*>(p) + i);
+    }
+    template <typename T>
+    __device__ __forceinline__ Vec read(int u) const {
+        uint4 w[kUnits<T>];
+#pragma unroll
+        for (int i = 0; i < kUnits<T>; ++i) w[i] = shared16(out + (u + i) * unit);
+        return unpack<T>(w);
+    }
+    // Units [u, u + n) of every stage, for a vector that is never copied.
+    __device__ __forceinline__ void clear(int u, int n) const {
+        for (uint32_t s = first;; s += stage) {
+            for (int i = 0; i < n; ++i)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(s + (u + i) * unit), "r"(0) : "memory");
+            if (s == last) break;
+        }
+    }
+};
+
+// A row's copy is committed `stages` - 1 rows ahead; the oldest has arrived.
+__device__ __forceinline__ void ring_wait(int stages) {
+    switch (stages) {
+        case 1: async_wait<0>(); break;
+        case 2: async_wait<1>(); break;
+        case 3: async_wait<2>(); break;
+        case 4: async_wait<3>(); break;
+        case 5: async_wait<4>(); break;
+        default: async_wait<5>(); break;
+    }
+}
+constexpr int kMaxStages = 6;
+
+// A team of threads shares a row: the whole block (WIDE; a multiple of 32 threads, at most 1024), or
+// `size` threads of a warp, a power of two (then several teams in a block).
 constexpr int kTeamScratch = 2 * 4 * 32;  // floats of shared memory for a block-wide team's sums
 
+template <bool WIDE>
 struct Team {
     int size;
-    float* scratch;  // kTeamScratch floats (block-wide teams)
-    int turn;        // which half of the scratch the next sum uses
+    float* scratch;  // kTeamScratch floats, zero before the first sum (a block-wide team)
+    int turn = 0;    // which half of the scratch the next sum uses
 
-    // Every value summed over the team, in a fixed order; each thread gets the sums.  Consecutive sums use
-    // the scratch's halves in turn: before a thread can write a half again, every thread has passed the
-    // other half's barrier and so has read this one.
-    template <int N>
-    __device__ __forceinline__ void sum(float (&v)[N]) {
-        static_assert(N <= 4, "scratch holds four values a warp");
-        if (size <= 32) {
-            for (int o = size >> 1; o > 0; o >>= 1)
-#pragma unroll
-                for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
-            return;
+    __device__ Team(int n, float* s) : size(n), scratch(s) {
+        if (WIDE) {
+            for (int i = threadIdx.x; i < kTeamScratch; i += blockDim.x) s[i] = 0.f;
+            __syncthreads();
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-            for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = size >> 5;
-        float* s = scratch + turn * (4 * 32);
-        turn ^= 1;
-        if (lane == 0)
-#pragma unroll
-            for (int n = 0; n < N; ++n) s[n * 32 + warp] = v[n];
-        __syncthreads();
-#pragma unroll
-        for (int n = 0; n < N; ++n) v[n] = lane < warps ? s[n * 32 + lane] : 0.f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-            for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
     }
     __device__ __forceinline__ void sync() const {
-        if (size <= 32) __syncwarp();
-        else __syncthreads();
+        if (WIDE) __syncthreads();
+        else __syncwarp();
+    }
+    static __device__ __forceinline__ float swap(float x, int o) { return __shfl_xor_sync(0xffffffffu, x, o); }
+
+    // Every value summed over the team, in a fixed order; each thread gets the sums.  In a warp, lanes that
+    // exchange two or four values keep half of them each time, so that four values cost six shuffles and
+    // end in eight lanes each.  Across warps: one write, one barrier, and each lane adds four warps' values.
+    // Consecutive sums use the scratch's halves in turn: before a thread can write a half again, every
+    // thread has passed the other half's barrier and so has read this one.
+    template <int N>
+    __device__ __forceinline__ void sum(float (&v)[N]) {
+        static_assert(N == 1 || N == 2 || N == 4, "");
+        if (!WIDE) {
+            for (int o = size >> 1; o > 0; o >>= 1)
+#pragma unroll
+                for (int n = 0; n < N; ++n) v[n] += swap(v[n], o);
+            return;
+        }
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        float k;
+        if constexpr (N == 4) {
+            const bool up = lane & 16, right = lane & 8;
+            const float a = (up ? v[2] : v[0]) + swap(up ? v[0] : v[2], 16);
+            const float b = (up ? v[3] : v[1]) + swap(up ? v[1] : v[3], 16);
+            k = (right ? b : a) + swap(right ? a : b, 8);
+        } else if constexpr (N == 2) {
+            const bool up = lane & 16;
+            k = (up ? v[1] : v[0]) + swap(up ? v[0] : v[1], 16);
+            k += swap(k, 8);
+        } else {
+            k = v[0] + swap(v[0], 16);
+            k += swap(k, 8);
+        }
+        k += swap(k, 4);
+        k += swap(k, 2);
+        k += swap(k, 1);
+        constexpr int span = 32 / N;  // lanes a value
+        float* s = scratch + turn * (4 * 32);
+        turn ^= 1;
+        if (lane % span == 0) s[lane / span * 32 + warp] = k;
+        __syncthreads();
+        const float4 u = reinterpret_cast<const float4*>(s)[lane / span * 8 + (lane & 7)];
+        k = (u.x + u.y) + (u.z + u.w);
+        k += swap(k, 4);
+        k += swap(k, 2);
+        k += swap(k, 1);
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] = N == 1 ? k : __shfl_sync(0xffffffffu, k, n * span);
     }
 };
 
@@ -169,6 +284,34 @@ struct Team {
 __host__ __device__ inline long long worker_lo(long long n, int workers, int w) { return n * w / workers; }
 __host__ __device__ inline int worker_of(long long n, int workers, long long r) {
     return static_cast<int>(((r + 1) * workers - 1) / n);
+}
+
+// Threads of a block for a row of `slots` vectors, with `V` vectors a thread: rows of up to 32 vectors
+// share a block of 128 threads.
+inline void row_team(int slots, int V, RowPlan* p) {
+    p->V = V;
+    if (slots <= 32) {
+        p->team = 1;
+        while (p->team < slots) p->team *= 2;
+        p->threads = 128;
+    } else {
+        p->team = p->threads = ((slots + V - 1) / V + 31) / 32 * 32;
+    }
+}
+// One worker a team; no more blocks than `most`, nor than rows.
+inline void row_workers(long long rows, int most, RowPlan* p) {
+    const int teams = p->threads / p->team;
+    const long long want = (rows + teams - 1) / teams, cap = kMaxWorkers / teams < most ? kMaxWorkers / teams : most;
+    p->blocks = static_cast<int>(want < cap ? want : cap);
+    p->workers = p->blocks * teams;
+}
+// Stages of a ring: enough that a processor's blocks keep 96 KB of copies in flight (about twice what its
+// share of the bandwidth moves in the time a load takes), within `room` bytes a block.
+inline int ring_stages(size_t stage, int blocks_per_sm, size_t room) {
+    int n = 2;
+    while (n < kMaxStages && (n - 1) * stage * blocks_per_sm < 96 * 1024) ++n;
+    while (n > 1 && n * stage > room) --n;
+    return n;
 }
 
 }  // namespace slra
