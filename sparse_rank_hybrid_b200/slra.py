@@ -10,8 +10,8 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
-from collections import namedtuple
 from dataclasses import dataclass, field
+from typing import NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libslra.so")
@@ -300,6 +300,7 @@ def layout(prob: Problem) -> Layout:
 
 
 # ------------------------------------------------------------------------------- torch helpers
+@functools.lru_cache(maxsize=None)
 def _torch():
     import torch
     return torch
@@ -558,74 +559,98 @@ def ws_view(prob: Problem, workspace, name: str):
 
 
 # ------------------------------------------------------------- operators around the attention
+# Single tokens make short calls, so what these functions do on the host is kept small: problems are
+# tuples, their C structs are made once, and only what a call changes is set.
+@functools.lru_cache(maxsize=None)
+def _codes():
+    torch = _torch()
+    return {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_F32, torch.float16: DTYPE_F16}
+
+
+@functools.lru_cache(maxsize=None)
+def _types():
+    return {code: t for t, code in _codes().items()}
+
+
 def _code(t) -> int:
+    code = _codes().get(t.dtype)
+    if code is None:
+        raise ValueError(f"expected bf16, fp16 or fp32, got {t.dtype}")
+    return code
+
+
+@functools.lru_cache(maxsize=None)
+def _current_stream():
+    """device -> handle of its current stream; the direct query where this torch has one (a fraction of the
+    time that making a Stream object takes)."""
     torch = _torch()
-    dt = t.dtype
-    if dt is torch.bfloat16:
-        return DTYPE_BF16
-    if dt is torch.float32:
-        return DTYPE_F32
-    if dt is torch.float16:
-        return DTYPE_F16
-    raise ValueError(f"expected bf16, fp16 or fp32, got {dt}")
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None:
+        return lambda device: raw(device.index)
+    return lambda device: torch.cuda.current_stream(device).cuda_stream
 
 
-def _torch_dtype(code):
-    torch = _torch()
-    return {DTYPE_BF16: torch.bfloat16, DTYPE_F32: torch.float32, DTYPE_F16: torch.float16}[code]
-
-
-class _Call:
-    """Runs a call with the tensors' device current, on `stream` (None: that device's current stream);
-    what it allocates then belongs to that stream."""
+class _On:
+    """The tensors' device made current, and `stream` (None: that device's current stream) with it; what is
+    allocated inside belongs to that stream.  Gives the stream's handle."""
+    __slots__ = ("ctx", "device")
 
     def __init__(self, device, stream):
         torch = _torch()
         if device.type != "cuda":
             raise ValueError(f"expected CUDA tensors, got {device}")
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-        self.ctx = None
-        if stream is not None or torch.cuda.current_device() != device.index:
-            self.ctx = torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device))
+        self.ctx, self.device = None, device
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+            self.ctx = torch.cuda.stream(stream)
+        elif torch.cuda.current_device() != device.index:
+            self.ctx = torch.cuda.stream(torch.cuda.current_stream(device))
 
     def __enter__(self):
         if self.ctx is not None:
             self.ctx.__enter__()
-        return int(_torch().cuda.current_stream().cuda_stream)
+        return _current_stream()(self.device)
 
     def __exit__(self, *exc):
         if self.ctx is not None:
             self.ctx.__exit__(*exc)
 
 
-def _expect(name, t, shape, dtype, device):
-    """A CUDA tensor of this shape (and type, where one is given), its last dimension contiguous."""
-    if not t.is_cuda or t.shape != shape or (dtype is not None and t.dtype is not dtype) or \
-            (t.stride(-1) != 1 and shape[-1] != 1):
-        raise ValueError(f"{name}: expected a CUDA {'' if dtype is None else str(dtype) + ' '}tensor of shape "
-                         f"{tuple(shape)} with a contiguous last dimension, got {t.dtype} {tuple(t.shape)} strides "
-                         f"{t.stride()} on {t.device}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-
-
-def _steps(t):
-    """Strides of the dimensions before the last one, (0, ...) when contiguous; a dimension of one element
-    gets any valid stride."""
-    if t.is_contiguous():
-        return (0,) * (t.dim() - 1)
-    return tuple(st if n > 1 else 8 for st, n in zip(t.stride()[:-1], t.shape[:-1]))
-
-
-def _dense(name, t, shape, dtype, device):
-    _expect(name, t, shape, dtype, device)
+def _rows(c, name, t, shape, dtype, device, field):
+    """Checks a tensor (type, where one is given, shape, device, contiguous last dimension), sets its strides
+    in the struct's `field` unless it is contiguous, and gives its address."""
+    if t.shape != shape or (dtype is not None and t.dtype is not dtype) or t.device != device:
+        raise ValueError(f"{name}: expected a {'' if dtype is None else str(dtype) + ' '}tensor of shape {tuple(shape)} on "
+                         f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     if not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
+        st = t.stride()
+        if st[-1] != 1 and shape[-1] != 1:
+            raise ValueError(f"{name}: expected a contiguous last dimension, got strides {st}")
+        # a dimension of one element gets any valid stride
+        getattr(c, field)[:] = [s if n > 1 else 8 for s, n in zip(st[:-1], shape)]
+    return t.data_ptr()
 
 
-@dataclass(frozen=True)
-class ResidualNorm:
+def _vector(name, t, n, dtype, device):
+    if t.shape != (n,) or (dtype is not None and t.dtype is not dtype) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {'' if dtype is None else str(dtype) + ' '}tensor of {n} elements "
+                         f"on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _sums_workspace(call, c, workspace, device):
+    """The caller's workspace, or one of the size the call needs (a problem that is refused gets a token
+    one: the call itself then says why)."""
+    torch = _torch()
+    if workspace is None:
+        return torch.empty(max(call(c), 256), dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous() or workspace.dtype is not torch.uint8:
+        raise ValueError(f"workspace: expected a contiguous uint8 tensor on {device}")
+    return workspace
+
+
+class ResidualNorm(NamedTuple):
     """Sizes and options of slra_residual_norm (see include/slra.h): x, y, x_out and h are
     [batch, tokens, channels], the modulation vectors [batch, groups, channels].  Types and strides are
     taken from the tensors of each call."""
@@ -640,12 +665,20 @@ class ResidualNorm:
     residual_scale: float = 1.0
 
 
-ResidualNormGrads = namedtuple("ResidualNormGrads",
-                               "dx dy dgate dscale dshift dweight dbias dpost_weight workspace")
+class ResidualNormGrads(NamedTuple):
+    dx: object
+    dy: object
+    dgate: object
+    dscale: object
+    dshift: object
+    dweight: object
+    dbias: object
+    dpost_weight: object
+    workspace: object
 
 
 @functools.lru_cache(maxsize=256)
-def _residual_norm_template(prob: ResidualNorm) -> bytes:
+def _residual_norm_template(prob: ResidualNorm):
     c = _ResidualNorm()
     _check(lib().slra_residual_norm_init(ctypes.byref(c), prob.batch, prob.tokens, prob.channels),
            "slra_residual_norm_init")
@@ -655,35 +688,39 @@ def _residual_norm_template(prob: ResidualNorm) -> bytes:
 
 
 def _residual_norm_problem(prob, x, y, h, gate, scale, shift, weight, bias, post_weight):
-    """The filled C struct from the tensors; h (or dh) may be None: the block type is then y's, or x's."""
+    """The struct filled from the tensors, the block type (that of y, h or dh, else x's), and the addresses
+    of x and y."""
     c = _ResidualNorm.from_buffer_copy(_residual_norm_template(prob))
-    row = (prob.batch, prob.tokens, prob.channels)
-    _expect("x", x, row, None, x.device)
+    device = x.device
+    batch, tokens, channels, groups = prob[:4]
+    row = (batch, tokens, channels)
     c.stream_dtype = _code(x)
-    c.x_strides[:] = _steps(x)
+    px = _rows(c, "x", x, row, None, device, "x_strides")
     block = y if y is not None else h if h is not None else x
     c.block_dtype = _code(block)
-    if y is not None:
-        _expect("y", y, row, None, x.device)
-        c.y_strides[:] = _steps(y)
-    dtype = None
+    py = None if y is None else _rows(c, "y", y, row, None, device, "y_strides")
+    mods, dtype = (batch, groups, channels), None
     for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
         if t is not None:
-            _expect(name, t, (prob.batch, prob.groups, prob.channels), dtype, x.device)
-            dtype = t.dtype
-            c.mod_dtype = _code(t)
+            if t.shape != mods or (dtype is not None and t.dtype is not dtype) or t.device != device or \
+                    (channels > 1 and t.stride(2) != 1):
+                raise ValueError(f"{name}: expected {mods} on {device} with a contiguous last dimension, of one type with "
+                                 f"the other modulation vectors, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on "
+                                 f"{t.device}")
+            if dtype is None:
+                dtype = t.dtype
+                c.mod_dtype = _code(t)
             setattr(c, name, t.data_ptr())
             if not t.is_contiguous():
-                getattr(c, name + "_strides")[:] = (t.stride(0) if prob.batch > 1 else 0,
-                                                    t.stride(1) if prob.groups > 1 else 0)
+                getattr(c, name + "_strides")[:] = (t.stride(0) if batch > 1 else 0, t.stride(1) if groups > 1 else 0)
     dtype = None
     for name, t in (("weight", weight), ("bias", bias), ("post_weight", post_weight)):
         if t is not None:
-            _dense(name, t, (prob.channels,), dtype, x.device)
-            dtype = t.dtype
-            c.weight_dtype = _code(t)
-            setattr(c, name, t.data_ptr())
-    return c, block.dtype
+            setattr(c, name, _vector(name, t, channels, dtype, device))
+            if dtype is None:
+                dtype = t.dtype
+                c.weight_dtype = _code(t)
+    return c, block.dtype, px, py
 
 
 def residual_norm_fwd(prob: ResidualNorm, x, y=None, gate=None, scale=None, shift=None, weight=None, bias=None,
@@ -694,32 +731,31 @@ def residual_norm_fwd(prob: ResidualNorm, x, y=None, gate=None, scale=None, shif
     (expanded views broadcast); weight, bias, post_weight: [channels].  h gets y's type, or h_dtype (a
     torch dtype; for a call without y, default x's).  Rows may be strided, x_out may be x and h may be y.
     Returns (x_out, h): x itself where there is no y, None for h with NORM_NONE."""
-    torch = _torch()
-    row = (prob.batch, prob.tokens, prob.channels)
-    c, block = _residual_norm_problem(prob, x, y, h, gate, scale, shift, weight, bias, post_weight)
-    if h_dtype is not None and y is None and h is None:
-        block = h_dtype
-        c.block_dtype = _code(torch.empty(0, dtype=h_dtype))
-    with _Call(x.device, stream) as handle:
-        if y is not None:
-            if x_out is None:
-                x_out = torch.empty(row, dtype=x.dtype, device=x.device)
-            else:
-                _expect("x_out", x_out, row, x.dtype, x.device)
-                c.x_out_strides[:] = _steps(x_out)
-        elif x_out is not None:
-            raise ValueError("x_out: there is no y to add")
-        if prob.norm != NORM_NONE:
-            if h is None:
-                h = torch.empty(row, dtype=block, device=x.device)
-            else:
-                _expect("h", h, row, block, x.device)
-                c.h_strides[:] = _steps(h)
-        elif h is not None:
-            raise ValueError("h: the problem has no norm")
-        _check(lib().slra_residual_norm_fwd(ctypes.byref(c), x.data_ptr(), None if y is None else y.data_ptr(),
-                                            None if y is None else x_out.data_ptr(),
-                                            None if h is None else h.data_ptr(), handle), "slra_residual_norm_fwd")
+    empty = _torch().empty
+    row, device = prob[:3], x.device
+    with _On(device, stream) as handle:
+        c, block, px, py = _residual_norm_problem(prob, x, y, h, gate, scale, shift, weight, bias, post_weight)
+        if h_dtype is not None and y is None and h is None:
+            block = h_dtype
+            c.block_dtype = _codes()[h_dtype]
+        po = ph = None
+        if y is None:
+            if x_out is not None:
+                raise ValueError("x_out: there is no y to add")
+        elif x_out is None:
+            x_out = empty(row, dtype=x.dtype, device=device)
+            po = x_out.data_ptr()
+        else:
+            po = _rows(c, "x_out", x_out, row, x.dtype, device, "x_out_strides")
+        if prob.norm == NORM_NONE:
+            if h is not None:
+                raise ValueError("h: the problem has no norm")
+        elif h is None:
+            h = empty(row, dtype=block, device=device)
+            ph = h.data_ptr()
+        else:
+            ph = _rows(c, "h", h, row, block, device, "h_strides")
+        _check(lib().slra_residual_norm_fwd(c, px, py, po, ph, handle), "slra_residual_norm_fwd")
     return (x if y is None else x_out), h
 
 
@@ -731,59 +767,38 @@ def residual_norm_bwd(prob: ResidualNorm, x, y=None, dh=None, dx_out=None, gate=
     dpost_weight [channels].  dx may be dx_out and dy may be dh.  workspace: a uint8 tensor to reuse (None:
     allocated; it comes back in the result).  Returns ResidualNormGrads, None where there is nothing."""
     torch = _torch()
-    row, mods, dev = (prob.batch, prob.tokens, prob.channels), (prob.batch, prob.groups, prob.channels), x.device
-    c, block = _residual_norm_problem(prob, x, y, dh, gate, scale, shift, weight, bias, post_weight)
-    if dh is not None:
-        _expect("dh", dh, row, block, dev)
-        c.h_strides[:] = _steps(dh)
-    if dx_out is not None:
-        _expect("dx_out", dx_out, row, x.dtype, dev)
-        c.x_out_strides[:] = _steps(dx_out)
-    with _Call(dev, stream) as handle:
+    empty, f32 = torch.empty, torch.float32
+    row, device = prob[:3], x.device
+    L = lib()
+    with _On(device, stream) as handle:
+        c, block, px, py = _residual_norm_problem(prob, x, y, dh, gate, scale, shift, weight, bias, post_weight)
+        pdh = None if dh is None else _rows(c, "dh", dh, row, block, device, "h_strides")
+        pdo = None if dx_out is None else _rows(c, "dx_out", dx_out, row, x.dtype, device, "x_out_strides")
         if dx is None:
-            dx = torch.empty(row, dtype=x.dtype, device=dev)
-        else:
-            _expect("dx", dx, row, x.dtype, dev)
-            c.dx_strides[:] = _steps(dx)
-        if y is None:
-            if dy is not None:
-                raise ValueError("dy: there is no y")
-        elif dy is None:
-            dy = torch.empty(row, dtype=block, device=dev)
-        else:
-            _expect("dy", dy, row, block, dev)
-            c.dy_strides[:] = _steps(dy)
-        out = {}
-        for name, t, shape in (("dgate", gate, mods), ("dscale", scale, mods), ("dshift", shift, mods),
-                               ("dweight", weight, mods[2:]), ("dbias", bias, mods[2:]),
-                               ("dpost_weight", post_weight, mods[2:])):
-            out[name] = None
+            dx = empty(row, dtype=x.dtype, device=device)
+        pdx, pdy = _rows(c, "dx", dx, row, x.dtype, device, "dx_strides"), None
+        if y is not None:
+            if dy is None:
+                dy = empty(row, dtype=block, device=device)
+            pdy = _rows(c, "dy", dy, row, block, device, "dy_strides")
+        elif dy is not None:
+            raise ValueError("dy: there is no y")
+        mods = (prob.batch, prob.groups, prob.channels)
+        out = []
+        for name, t in (("dgate", gate), ("dscale", scale), ("dshift", shift), ("dweight", weight), ("dbias", bias),
+                        ("dpost_weight", post_weight)):
+            g = None
             if t is not None:
-                out[name] = torch.empty(shape, dtype=torch.float32, device=dev)
-                setattr(c, name, out[name].data_ptr())
-        workspace = _sums_workspace("slra_residual_norm_bwd", c, workspace, dev)
-        _check(lib().slra_residual_norm_bwd(ctypes.byref(c), x.data_ptr(), None if y is None else y.data_ptr(),
-                                            None if dx_out is None else dx_out.data_ptr(),
-                                            None if dh is None else dh.data_ptr(), dx.data_ptr(),
-                                            None if dy is None else dy.data_ptr(), workspace.data_ptr(),
-                                            workspace.numel(), handle), "slra_residual_norm_bwd")
-    return ResidualNormGrads(dx, dy, workspace=workspace, **out)
+                g = empty(mods if t.dim() == 3 else mods[2:], dtype=f32, device=device)
+                setattr(c, name, g.data_ptr())
+            out.append(g)
+        workspace = _sums_workspace(L.slra_residual_norm_bwd_workspace_bytes, c, workspace, device)
+        _check(L.slra_residual_norm_bwd(c, px, py, pdo, pdh, pdx, pdy, workspace.data_ptr(), workspace.numel(), handle),
+               "slra_residual_norm_bwd")
+    return ResidualNormGrads(dx, dy, *out, workspace)
 
 
-def _sums_workspace(call, c, workspace, device):
-    """The caller's workspace, or one of the size the call needs (a problem that is refused gets a token
-    one: the call itself then says why)."""
-    if workspace is None:
-        n = getattr(lib(), call + "_workspace_bytes")(ctypes.byref(c))
-        return _torch().empty(max(n, 256), dtype=_torch().uint8, device=device)
-    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous() or \
-            workspace.element_size() != 1:
-        raise ValueError(f"workspace: expected a contiguous uint8 tensor on {device}")
-    return workspace
-
-
-@dataclass(frozen=True)
-class QkRope:
+class QkRope(NamedTuple):
     """Sizes and options of slra_qk_rope (see include/slra.h): q is [batch, tokens, heads, head_dim], k the
     same with kv_heads.  Types and strides are taken from the tensors of each call."""
     batch: int
@@ -804,11 +819,16 @@ class QkRope:
     out_dtype: int = None            # of the forward's outputs, DTYPE_*; None: q's
 
 
-QkRopeGrads = namedtuple("QkRopeGrads", "dq dk dwq dwk workspace")
+class QkRopeGrads(NamedTuple):
+    dq: object
+    dk: object
+    dwq: object
+    dwk: object
+    workspace: object
 
 
 @functools.lru_cache(maxsize=256)
-def _qk_rope_template(prob: QkRope) -> bytes:
+def _qk_rope_template(prob: QkRope):
     c = _QkRope()
     _check(lib().slra_qk_rope_init(ctypes.byref(c), prob.batch, prob.tokens, prob.heads, prob.head_dim),
            "slra_qk_rope_init")
@@ -821,24 +841,32 @@ def _qk_rope_template(prob: QkRope) -> bytes:
     return bytes(c)
 
 
-def _qk_rope_problem(prob, wq, wk, positions, device):
-    torch = _torch()
+def _qk_rope_problem(prob, q, k, wq, wk, positions):
+    """The struct filled from the inputs, and the addresses of q and k."""
     c = _QkRope.from_buffer_copy(_qk_rope_template(prob))
-    dtype = None
-    for name, w, heads in (("wq", wq, prob.heads), ("wk", wk, prob.kv_heads)):
-        if w is not None:
-            _dense(name, w, ((heads if prob.norm == QK_NORM_TOKEN else 1) * prob.head_dim,), dtype, device)
-            dtype = w.dtype
-            c.weight_dtype = _code(w)
-            setattr(c, name, w.data_ptr())
+    device = q.device
+    batch, tokens, heads, D, kv_heads = prob[:5]
+    if (k is not None) != (kv_heads > 0):
+        raise ValueError(f"k: the problem has {kv_heads} key heads")
+    c.x_dtype = _code(q)
+    pq = _rows(c, "q", q, (batch, tokens, heads, D), None, device, "q_strides")
+    pk = None if k is None else _rows(c, "k", k, (batch, tokens, kv_heads, D), q.dtype, device, "k_strides")
+    token = prob.norm == QK_NORM_TOKEN
+    if wq is not None:
+        c.wq = _vector("wq", wq, heads * D if token else D, None, device)
+        c.weight_dtype = _code(wq)
+    if wk is not None:
+        c.wk = _vector("wk", wk, kv_heads * D if token else D, None if wq is None else wq.dtype, device)
+        c.weight_dtype = _code(wk)
     if positions is not None:
-        if positions.dim() != 3 or positions.shape[0] not in (1, prob.batch) or \
-                (prob.tokens > 1 and positions.stride(1) != 3):
-            raise ValueError(f"positions: expected int32 [1 or {prob.batch}, {prob.tokens}, 3], every sample contiguous")
-        _expect("positions", positions, (positions.shape[0], prob.tokens, 3), torch.int32, device)
+        n, st = positions.shape[0], positions.stride()
+        if positions.shape != (n, tokens, 3) or n not in (1, batch) or positions.dtype is not _torch().int32 or \
+                positions.device != device or st[2] != 1 or (tokens > 1 and st[1] != 3):
+            raise ValueError(f"positions: expected int32 [1 or {batch}, {tokens}, 3] on {device}, every sample contiguous, "
+                             f"got {positions.dtype} {tuple(positions.shape)} strides {st} on {positions.device}")
         c.positions = positions.data_ptr()
-        c.positions_stride = positions.stride(0) if positions.shape[0] > 1 else 0
-    return c
+        c.positions_stride = st[0] if n > 1 else 0
+    return c, pq, pk
 
 
 def qk_rope_fwd(prob: QkRope, q, k=None, wq=None, wk=None, positions=None, out_q=None, out_k=None, stream=None):
@@ -846,34 +874,26 @@ def qk_rope_fwd(prob: QkRope, q, k=None, wq=None, wk=None, positions=None, out_q
     contiguous last dimension, e.g. views of a fused QKV tensor); wq, wk: the norm's weights ([head_dim], or
     [heads * head_dim] with QK_NORM_TOKEN); positions: int32 [1 or batch, tokens, 3] in place of the grid.
     out_q may be q and out_k may be k.  Returns (out_q, out_k); out_k is None without k."""
-    torch = _torch()
-    c = _qk_rope_problem(prob, wq, wk, positions, q.device)
-    c.x_dtype = _code(q)
-    c.out_dtype = c.x_dtype if prob.out_dtype is None else prob.out_dtype
-    out_dtype = q.dtype if prob.out_dtype is None else _torch_dtype(prob.out_dtype)
-    if (k is not None) != (prob.kv_heads > 0):
-        raise ValueError(f"k: the problem has {prob.kv_heads} key heads")
-    outs = []
-    with _Call(q.device, stream) as handle:
-        for n, t, o, heads in (("q", q, out_q, prob.heads), ("k", k, out_k, prob.kv_heads)):
-            if t is None:
-                if o is not None:
-                    raise ValueError(f"out_{n}: there is no {n}")
-                outs.append(None)
-                continue
-            shape = (prob.batch, prob.tokens, heads, prob.head_dim)
-            _expect(n, t, shape, q.dtype, q.device)
-            getattr(c, n + "_strides")[:] = _steps(t)
-            if o is None:
-                o = torch.empty(shape, dtype=out_dtype, device=q.device)
-            else:
-                _expect("out_" + n, o, shape, out_dtype, q.device)
-                getattr(c, f"out_{n}_strides")[:] = _steps(o)
-            outs.append(o)
-        _check(lib().slra_qk_rope_fwd(ctypes.byref(c), q.data_ptr(), None if k is None else k.data_ptr(),
-                                      outs[0].data_ptr(), None if k is None else outs[1].data_ptr(), handle),
-               "slra_qk_rope_fwd")
-    return tuple(outs)
+    empty = _torch().empty
+    device = q.device
+    with _On(device, stream) as handle:
+        c, pq, pk = _qk_rope_problem(prob, q, k, wq, wk, positions)
+        code = prob.out_dtype
+        dtype = q.dtype if code is None else _types()[code]
+        c.out_dtype = c.x_dtype if code is None else code
+        shape, po_k = (prob.batch, prob.tokens, prob.heads, prob.head_dim), None
+        if out_q is None:
+            out_q = empty(shape, dtype=dtype, device=device)
+        po_q = _rows(c, "out_q", out_q, shape, dtype, device, "out_q_strides")
+        if k is not None:
+            shape = (prob.batch, prob.tokens, prob.kv_heads, prob.head_dim)
+            if out_k is None:
+                out_k = empty(shape, dtype=dtype, device=device)
+            po_k = _rows(c, "out_k", out_k, shape, dtype, device, "out_k_strides")
+        elif out_k is not None:
+            raise ValueError("out_k: there is no k")
+        _check(lib().slra_qk_rope_fwd(c, pq, pk, po_q, po_k, handle), "slra_qk_rope_fwd")
+    return out_q, out_k
 
 
 def qk_rope_bwd(prob: QkRope, q, k, dout_q, dout_k=None, wq=None, wk=None, positions=None, dq=None, dk=None,
@@ -883,36 +903,34 @@ def qk_rope_bwd(prob: QkRope, q, k, dout_q, dout_k=None, wq=None, wk=None, posit
     given (e.g. views of one fused gradient, or dout_q, dout_k themselves where the types agree).
     workspace: as for residual_norm_bwd.  Returns QkRopeGrads, None where there is nothing."""
     torch = _torch()
-    c = _qk_rope_problem(prob, wq, wk, positions, q.device)
-    c.x_dtype, c.out_dtype = _code(q), _code(dout_q)
-    if (k is not None) != (prob.kv_heads > 0) or (dout_k is not None) != (prob.kv_heads > 0):
-        raise ValueError(f"k, dout_k: the problem has {prob.kv_heads} key heads")
-    grads, weights = [], []
-    with _Call(q.device, stream) as handle:
-        for n, t, d, o, heads, w in (("q", q, dout_q, dq, prob.heads, wq), ("k", k, dout_k, dk, prob.kv_heads, wk)):
-            if t is None:
-                if o is not None:
-                    raise ValueError(f"d{n}: there is no {n}")
-                grads.append(None)
-                weights.append(None)
-                continue
-            shape = (prob.batch, prob.tokens, heads, prob.head_dim)
-            _expect(n, t, shape, q.dtype, q.device)
-            getattr(c, n + "_strides")[:] = _steps(t)
-            _expect("dout_" + n, d, shape, dout_q.dtype, q.device)
-            getattr(c, f"out_{n}_strides")[:] = _steps(d)
-            if o is None:
-                o = torch.empty(shape, dtype=q.dtype, device=q.device)
-            else:
-                _expect("d" + n, o, shape, q.dtype, q.device)
-                getattr(c, f"d{n}_strides")[:] = _steps(o)
-            grads.append(o)
-            weights.append(None if w is None else torch.empty(w.shape, dtype=torch.float32, device=q.device))
-            if w is not None:
-                setattr(c, f"dw{n}", weights[-1].data_ptr())
-        workspace = _sums_workspace("slra_qk_rope_bwd", c, workspace, q.device)
-        _check(lib().slra_qk_rope_bwd(ctypes.byref(c), q.data_ptr(), None if k is None else k.data_ptr(),
-                                      dout_q.data_ptr(), None if k is None else dout_k.data_ptr(), grads[0].data_ptr(),
-                                      None if k is None else grads[1].data_ptr(), workspace.data_ptr(),
-                                      workspace.numel(), handle), "slra_qk_rope_bwd")
-    return QkRopeGrads(grads[0], grads[1], weights[0], weights[1], workspace)
+    empty, f32 = torch.empty, torch.float32
+    device = q.device
+    L = lib()
+    if (dout_k is not None) != (prob.kv_heads > 0):
+        raise ValueError(f"dout_k: the problem has {prob.kv_heads} key heads")
+    with _On(device, stream) as handle:
+        c, pq, pk = _qk_rope_problem(prob, q, k, wq, wk, positions)
+        c.out_dtype = _code(dout_q)
+        shape, dwq, dwk, pgk, pdk = (prob.batch, prob.tokens, prob.heads, prob.head_dim), None, None, None, None
+        pgq = _rows(c, "dout_q", dout_q, shape, None, device, "out_q_strides")
+        if dq is None:
+            dq = empty(shape, dtype=q.dtype, device=device)
+        pdq = _rows(c, "dq", dq, shape, q.dtype, device, "dq_strides")
+        if k is not None:
+            shape = (prob.batch, prob.tokens, prob.kv_heads, prob.head_dim)
+            pgk = _rows(c, "dout_k", dout_k, shape, dout_q.dtype, device, "out_k_strides")
+            if dk is None:
+                dk = empty(shape, dtype=q.dtype, device=device)
+            pdk = _rows(c, "dk", dk, shape, q.dtype, device, "dk_strides")
+        elif dk is not None:
+            raise ValueError("dk: there is no k")
+        if wq is not None:
+            dwq = empty(wq.shape, dtype=f32, device=device)
+            c.dwq = dwq.data_ptr()
+        if wk is not None:
+            dwk = empty(wk.shape, dtype=f32, device=device)
+            c.dwk = dwk.data_ptr()
+        workspace = _sums_workspace(L.slra_qk_rope_bwd_workspace_bytes, c, workspace, device)
+        _check(L.slra_qk_rope_bwd(c, pq, pk, pgq, pgk, pdq, pdk, workspace.data_ptr(), workspace.numel(), handle),
+               "slra_qk_rope_bwd")
+    return QkRopeGrads(dq, dk, dwq, dwk, workspace)

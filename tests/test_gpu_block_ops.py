@@ -330,8 +330,8 @@ def test_norm_deterministic_streams_and_graphs():
     assert all(torch.equal(getattr(other, n), getattr(ref, n)) for n in names)
     assert torch.equal(f[0], f_other[0]) and torch.equal(f[1], f_other[1])
     # the library's own workspace: NULL
-    c, _ = slra._residual_norm_problem(p, t["x"], t["y"], d["dh"], *(t[n] for n in ("gate", "scale", "shift", "weight",
-                                                                                  "bias", "post_weight")))
+    c = slra._residual_norm_problem(p, t["x"], t["y"], d["dh"], *(t[n] for n in ("gate", "scale", "shift", "weight",
+                                                                                  "bias", "post_weight")))[0]
     own = {n: torch.empty_like(getattr(ref, n)) for n in names}
     for n in names[2:]:
         setattr(c, n, own[n].data_ptr())
@@ -617,7 +617,8 @@ def test_rope_deterministic_streams_and_graphs(norm):
     for n in names:
         assert torch.equal(getattr(other, n), getattr(ref, n)) and torch.equal(getattr(again, n), getattr(ref, n))
     assert torch.equal(fo[0], f[0]) and torch.equal(fo[1], f[1])
-    c = slra._qk_rope_problem(p, t["wq"], t["wk"], None, t["q"].device)
+    c = slra._qk_rope_problem(p, t["q"], t["k"], t["wq"], t["wk"], None)[0]
+    c.out_dtype = c.x_dtype
     own = {n: torch.empty_like(getattr(ref, n)) for n in names}
     c.dwq, c.dwk = own["dwq"].data_ptr(), own["dwk"].data_ptr()
     assert slra.lib().slra_qk_rope_bwd(ctypes.byref(c), t["q"].data_ptr(), t["k"].data_ptr(), d["dout_q"].data_ptr(),
