@@ -1,5 +1,6 @@
 // C ABI of the operators around the attention (declared in include/slra.h): argument validation and
 // launches of residual_norm.cu and qk_rope.cu.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -210,7 +211,7 @@ slra_status derive(const slra_qk_rope* p, Heads* d) {
         return SLRA_ERR_INVALID_ARG;
     if (!known_dtype(p->x_dtype) || !known_dtype(p->out_dtype) || !known_dtype(p->weight_dtype) || !positive(p->eps))
         return SLRA_ERR_INVALID_ARG;
-    if (p->theta < 0.0 || !std::isfinite(p->theta)) return SLRA_ERR_INVALID_ARG;
+    if (!(p->theta == 0.0 || p->theta >= 1.0) || !std::isfinite(p->theta)) return SLRA_ERR_INVALID_ARG;
     if (p->norm == SLRA_QK_NORM_NONE && (p->wq || p->wk)) return SLRA_ERR_INVALID_ARG;
     if ((p->dwq && !p->wq) || (p->dwk && !p->wk) || (p->wk && p->kv_heads == 0)) return SLRA_ERR_INVALID_ARG;
     if (p->rotate) {
@@ -221,7 +222,7 @@ slra_status derive(const slra_qk_rope* p, Heads* d) {
         } else {
             if (p->T < 1 || p->H < 1 || p->W < 1 || p->T >= most || p->H >= most || p->W >= most || p->first_token < 0)
                 return SLRA_ERR_INVALID_ARG;
-            if (p->H * p->W >= most || p->T * (p->H * p->W) < p->tokens ||
+            if (p->H * p->W >= most || p->T * (p->H * p->W) >= most || p->T * (p->H * p->W) < p->tokens ||
                 p->first_token > p->T * (p->H * p->W) - p->tokens)
                 return SLRA_ERR_INVALID_ARG;
         }
@@ -231,7 +232,7 @@ slra_status derive(const slra_qk_rope* p, Heads* d) {
     if (p->head_dim % 8 != 0 || p->head_dim > 256) return SLRA_ERR_UNSUPPORTED;
     int64_t g = 1;
     while (g * 8 < p->head_dim) g *= 2;
-    if (p->heads > 2048 || p->kv_heads > 2048 || (p->heads + p->kv_heads) * g > 2048) return SLRA_ERR_UNSUPPORTED;
+    if (p->heads > 1024 || p->kv_heads > 1024 || p->heads * g > 1024 || p->kv_heads * g > 1024) return SLRA_ERR_UNSUPPORTED;
     if (p->out_dtype != p->x_dtype && p->out_dtype != SLRA_DTYPE_F32) return SLRA_ERR_UNSUPPORTED;
     for (const void* v : {p->wq, p->wk, static_cast<const void*>(p->dwq), static_cast<const void*>(p->dwk)})
         if (!aligned16(v)) return SLRA_ERR_ALIGNMENT;
@@ -242,6 +243,8 @@ slra_status derive(const slra_qk_rope* p, Heads* d) {
         !strides_of(p->out_q_strides, L, hq, D, O, &d->out_q) || !strides_of(p->out_k_strides, L, hk, D, O, &d->out_k) ||
         !strides_of(p->dq_strides, L, hq, D, X, &d->dq) || !strides_of(p->dk_strides, L, hk, D, X, &d->dk))
         return SLRA_ERR_INVALID_ARG;
+    for (const Strides* st : {&d->q, &d->k, &d->out_q, &d->out_k, &d->dq, &d->dk})  // 32-bit places in a token
+        if ((std::max(hq, hk) - 1) * st->h + D >= most) return SLRA_ERR_UNSUPPORTED;
 
     QkRopeArgs& a = d->a;
     std::memset(&a, 0, sizeof a);
@@ -270,16 +273,23 @@ slra_status derive(const slra_qk_rope* p, Heads* d) {
         } else {
             for (int i = 0; i < 3; ++i) split[i] = p->rope_split[i];
         }
+        // omega / 2 pi = theta^(-m / n) / 2 pi in units of 2^-64 turns: powers of one ratio an axis, in long
+        // double so that their products stay below a rounding of double
         const int64_t n = split[0] + split[1] + split[2];
-        const double theta = p->theta > 0.0 ? p->theta : 10000.0, two_pi = 6.283185307179586476925;
+        const long double ln = std::log(static_cast<long double>(p->theta > 0.0 ? p->theta : 10000.0));
+        const long double first = 0x1p64L / 6.283185307179586476925286767L;
+        long double turns = first;
         int j = 0;
-        for (int ax = 0; ax < 3; ++ax)
-            for (int64_t m = 0; m < split[ax]; ++m, ++j) {
-                const double power = p->schedule == SLRA_ROPE_SHARED ? static_cast<double>(j) / n
-                                                                     : static_cast<double>(m) / split[ax];
-                a.turns[j] = std::pow(theta, -power) / two_pi;
+        for (int ax = 0; ax < 3; ++ax) {
+            if (split[ax] == 0) continue;
+            const bool shared = p->schedule == SLRA_ROPE_SHARED;
+            const long double ratio = std::exp(-ln / (shared ? n : split[ax]));
+            if (!shared) turns = first;
+            for (int64_t m = 0; m < split[ax]; ++m, ++j, turns *= ratio) {
+                a.turns[j] = static_cast<uint64_t>(turns);
                 a.axis[j] = static_cast<uint8_t>(ax);
             }
+        }
         a.positions = p->positions;
         a.positions_b = p->positions_stride;
         a.first = p->first_token;
@@ -289,8 +299,9 @@ slra_status derive(const slra_qk_rope* p, Heads* d) {
     }
     d->bytes = 256;
     if (p->dwq || p->dwk) {
-        const RowPlan plan = qk_rope_plan(a.rows, a.head_dim, a.side[0].heads + a.side[1].heads, true);
-        const int64_t columns = p->norm == SLRA_QK_NORM_TOKEN ? (p->heads + p->kv_heads) * D : (p->kv_heads ? 2 : 1) * D;
+        const RowPlan plan = qk_rope_plan(a.rows, a.head_dim, a.side[0].heads, a.side[1].heads, a.norm, true);
+        const int64_t columns =
+            p->norm == SLRA_QK_NORM_TOKEN ? (p->heads + p->kv_heads) * D : (p->kv_heads ? 2 : 1) * D * plan.parts;
         d->bytes = align_up(static_cast<size_t>(plan.workers) * columns * sizeof(float), 256);
     }
     return SLRA_OK;

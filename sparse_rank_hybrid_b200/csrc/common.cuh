@@ -273,9 +273,10 @@ constexpr int kMaxWorkers = 32768;  // teams of threads that share a call's rows
 constexpr int kNormNone = 0, kNormRms = 1, kNormLayer = 2;  // slra_norm
 
 // How a call's rows are shared out: `V` vectors of eight elements a thread, `team` threads a row,
-// `blocks` blocks of `threads` threads, `workers` teams in all.
+// `workers` teams in all, in blocks of `threads` threads.  A row may be cut into `parts` that different blocks
+// take (`blocks` = parts times those that hold the workers).
 struct RowPlan {
-    int V, team, threads, blocks, workers;
+    int V, team, threads, blocks, workers, parts;
 };
 
 struct RowTensor {  // [B][L][C], C contiguous; element strides of batch and token
@@ -314,6 +315,8 @@ struct RopeSide {
     const void* d;  // backward: gradient of the output
     void* out;      // forward: the output; backward: the gradient of x
     Strides sx, sd, so;
+    // bytes to the next token, and from behind a sample's last token to the next sample (set by the launcher)
+    long long next_x, next_d, next_o, wrap_x, wrap_d, wrap_o;
     const void* weight;  // [D] (norm per head) or [heads * D]; null: 1
     float* dweight;      // backward; null: not wanted
     int heads;
@@ -324,17 +327,19 @@ struct QkRopeArgs {
     long long positions_b;     // elements between samples
     long long rows, first;     // B * L; first token of the grid
     int tokens, head_dim;
-    int H, W;                  // grid (t is unbounded here)
+    int H, W;                  // grid
     long long offset[3];
     int rotate, halves, norm;
     int x_dtype, out_dtype, w_dtype;
     float eps;
-    float* part;  // [workers][sum of the weights' elements]: the weights' sums (null: none is wanted)
-    double turns[kRopeMaxPairs];   // omega / (2 pi) per pair, 0 for a pair that is not rotated
+    float* part;  // the weights' sums (null: none is wanted): norm over a token's heads [workers][heads * D of
+                  // both sides], norm per head [workers][parts][sides][D]
+    uint64_t turns[kRopeMaxPairs];  // omega / (2 pi) per pair in units of 2^-64, 0 for a pair that is not rotated
     uint8_t axis[kRopeMaxPairs];
-    int group, team, workers, stages;  // set by the launcher
+    // set by the launcher
+    int group, team, workers, stages, parts, split_sides, part_heads[2];
 };
-RowPlan qk_rope_plan(long long rows, int head_dim, int heads, bool backward);
+RowPlan qk_rope_plan(long long rows, int head_dim, int q_heads, int k_heads, int norm, bool backward);
 cudaError_t launch_qk_rope(const QkRopeArgs& a, bool backward, cudaStream_t st);
 
 }  // namespace slra

@@ -9,10 +9,11 @@
 // Bound by memory.  A team of threads takes all heads of a token's q and k together: thread and vector
 // of eight elements have a fixed (head, place in the head) for every token, so the weights and the
 // gradient sums of the weights stay in registers, and the token's angles are computed once for all heads.
-// The angle is a product in double (turns = omega / 2 pi per position), of which only the fraction of a
-// turn goes on to fp32: positions of any size keep an error below 1e-7 of a turn.  The table of a token's
-// cos and sin is filled while the token before it is computed.  Rows travel through a per-thread ring of
-// asynchronous copies as in residual_norm.cu.
+// The angle is counted in turns as an integer: position times omega / 2 pi in units of 2^-64 of a turn wraps
+// around at whole turns by itself, so its upper half is the fraction of a turn to 2^-32 wherever the
+// position is, for three integer multiplications (a double product with its rounding to a whole number took
+// most of the time of a step).  The table of a step's cos and sin is filled during the step before it.  Rows
+// travel through a per-thread ring of asynchronous copies as in residual_norm.cu.
 #include <algorithm>
 #include <type_traits>
 
@@ -23,41 +24,16 @@ namespace {
 
 constexpr size_t kRingBytes = 200 * 1024;  // dynamic shared memory of an SM's blocks at most
 
-constexpr int rope_threads(int V) { return V == 1 ? 1024 : V == 2 ? 640 : 512; }
+// Tokens that a team takes at a time, for V vectors a thread: what a step costs besides its vectors (the
+// loop, the ring, the table, the barrier and the sums' exchanges) is shared by them, while the weights and
+// their gradients' sums stay in the same registers.  The backward has registers for two vectors in all.
+template <int V, bool BWD>
+constexpr int kRows = BWD && V > 1 ? 1 : 2;
 
-// Eight elements of a head: consecutive ones (interleaved pairs), or four of the lower half and the four
-// they pair with in the upper half, `half` elements on.
-template <typename T, bool HALVES>
-__device__ __forceinline__ void copy_in(const Ring& ring, int u, const T* p, int half) {
-    if constexpr (!HALVES) {
-        ring.copy(u, p);
-    } else if constexpr (sizeof(T) == 4) {
-        async_copy16(ring.in + u * ring.unit, p);
-        async_copy16(ring.in + (u + 1) * ring.unit, p + half);
-    } else {
-        async_copy8(ring.in + u * ring.unit, p);
-        async_copy8(ring.in + u * ring.unit + 8, p + half);
-    }
-}
-template <typename T, bool HALVES>
-__device__ __forceinline__ void store_out(T* p, int half, const Vec& v) {
-    uint4 u[kUnits<T>];
-    pack<T>(v, u);
-    if constexpr (!HALVES) {
-#pragma unroll
-        for (int i = 0; i < kUnits<T>; ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
-    } else if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<uint4*>(p) = u[0];
-        *reinterpret_cast<uint4*>(p + half) = u[1];
-    } else {
-        *reinterpret_cast<uint2*>(p) = make_uint2(u[0].x, u[0].y);
-        *reinterpret_cast<uint2*>(p + half) = make_uint2(u[0].z, u[0].w);
-    }
-}
-__device__ __forceinline__ float weight_at(const void* w, int dtype, int at) {
-    return dtype == kF32    ? static_cast<const float*>(w)[at]
-           : dtype == kBf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[at])
-                            : __half2float(static_cast<const __half*>(w)[at]);
+// Threads of a block at most, so that the registers hold V vectors of kRows tokens with their weights and,
+// in the backward, the weights' sums.
+constexpr int rope_threads(int V, bool backward) {
+    return V == 1 ? 640 : V == 2 ? (backward ? 512 : 640) : (backward ? 320 : 512);
 }
 
 // The four pairs of a vector turned by their angles; the cos and sin of pairs (0, 1) and (2, 3) in c, s.
@@ -80,263 +56,298 @@ __device__ __forceinline__ void rotate(Vec& v, const float2 (&c)[2], const float
     }
 }
 
-template <typename TX, typename TO, int V, bool HALVES, bool BWD, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? rope_threads(V) : 128) qk_rope_kernel(const __grid_constant__ QkRopeArgs a) {
-    constexpr int UX = kUnits<TX>, UD = BWD ? kUnits<TO> : 0, ONE = UX + UD, U = V * ONE;
+// A head's eight elements are consecutive (interleaved pairs) or four of each half (SPLIT).  Of a thread's
+// vectors VQ are of q and VK of k; without the latter they are of the side that the block takes.
+template <typename TX, typename TO, int VQ, int VK, bool SPLIT, bool BWD, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? rope_threads(VQ + VK, BWD) : 128)
+    qk_rope_kernel(const __grid_constant__ QkRopeArgs a) {
+    constexpr int V = VQ + VK, R = kRows<V, BWD>;
+    constexpr int UX = kUnits<TX>, UD = BWD ? kUnits<TO> : 0, ONE = UX + UD, U = R * V * ONE;
     using TW = typename std::conditional<BWD, TX, TO>::type;  // type of what is written
     extern __shared__ uint4 shared[];
     __shared__ __align__(16) float scratch[kTeamScratch];
-    __shared__ double turns[kRopeMaxPairs];
+    __shared__ unsigned long long turns[kRopeMaxPairs];
     __shared__ int axis[kRopeMaxPairs];
-    const int D = a.head_dim, pairs = D / 2, half = HALVES ? D / 2 : 0, G = a.group;
+    const int D = a.head_dim, pairs = D / 2, gap = SPLIT ? D / 2 : 4, G = a.group;
     const int team_size = WIDE ? blockDim.x : a.team;
-    const int t = WIDE ? threadIdx.x : threadIdx.x % a.team, lane = t % G;
+    const int t = WIDE ? threadIdx.x : threadIdx.x % a.team, lane = t % G, c0 = lane * (SPLIT ? 4 : 8);
     const int in_block = WIDE ? 0 : threadIdx.x / a.team, teams = WIDE ? 1 : blockDim.x / a.team;
-    const int worker = blockIdx.x * teams + in_block;
-    const int q_heads = a.side[0].heads, heads = q_heads + a.side[1].heads;
+    const int part = blockIdx.x % a.parts, worker = blockIdx.x / a.parts * teams + in_block;
     for (int j = threadIdx.x; j < pairs; j += blockDim.x) turns[j] = a.turns[j], axis[j] = a.axis[j];
     Team<WIDE> team(team_size, scratch);
     __syncthreads();
-    // cos and sin of the current and the next token: [2][2][pairs] floats a team, behind the ring
-    float* table = reinterpret_cast<float*>(shared + static_cast<size_t>(a.stages) * U * blockDim.x) + in_block * 4 * pairs;
+    // cos and sin of this step's and the next one's tokens: [2][R][2][pairs] floats a team, behind the ring
+    float* table = reinterpret_cast<float*>(shared + static_cast<size_t>(a.stages) * U * blockDim.x) + in_block * 4 * R * pairs;
 
     const long long r0 = worker_lo(a.rows, a.workers, worker), r1 = worker_lo(a.rows, a.workers, worker + 1);
     const int n = static_cast<int>(r1 - r0);
-    const int iters = WIDE ? n : static_cast<int>((a.rows + a.workers - 1) / a.workers);
+    // teams of one warp take part in each other's shuffles, so they all loop as long as the longest
+    const int longest = WIDE ? n : static_cast<int>((a.rows + a.workers - 1) / a.workers);
     const int b0 = static_cast<int>(r0 / a.tokens), l0 = static_cast<int>(r0 % a.tokens);
     const bool need_x = !BWD || a.norm != kQkNormNone;
 
-    // this thread's vectors: which side and head, where, and whether there is one
+    // this block's heads of each side, and this thread's vectors: the head, and where it is in a token
+    const int piece = a.split_sides ? 0 : part, side_q = VK == 0 && a.split_sides ? part : 0;
     Ring ring(shared_address(shared), a.stages, U);
-    const TX* px[V];
-    const TO* pd[V];
-    TW* po[V];
+    int head[V];
+    bool on[V];
+    const char *px[V], *pd[V];
+    char* po[V];
     Vec w[V], dw[V];
-    bool is_k[V], on[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int head = (t + v * team_size) / G;
-        on[v] = head < heads && lane * 8 < D;
-        is_k[v] = head >= q_heads;
-        const RopeSide& s = a.side[is_k[v]];
-        const int h = on[v] ? head - (is_k[v] ? q_heads : 0) : 0, c = lane * (HALVES ? 4 : 8);
-        px[v] = static_cast<const TX*>(s.x) + s.sx.row(b0, l0, h) + c;
-        pd[v] = static_cast<const TO*>(s.d) + s.sd.row(b0, l0, h) + c;
-        po[v] = static_cast<TW*>(s.out) + s.so.row(b0, l0, h) + c;
-        if (!on[v]) ring.clear(v * ONE, ONE);
+        const int side = v < VQ ? side_q : 1;
+        const RopeSide& s = a.side[side];
+        const int first = piece * a.part_heads[side], last = min(s.heads, first + a.part_heads[side]);
+        head[v] = first + (t + (v < VQ ? v : v - VQ) * team_size) / G;
+        on[v] = head[v] < last && lane * 8 < D;
+        if (!on[v]) head[v] = 0;
+        px[v] = static_cast<const char*>(s.x) + (s.sx.row(b0, l0, head[v]) + c0) * static_cast<int>(sizeof(TX));
+        pd[v] = static_cast<const char*>(s.d) + (s.sd.row(b0, l0, head[v]) + c0) * static_cast<int>(sizeof(TO));
+        po[v] = static_cast<char*>(s.out) + (s.so.row(b0, l0, head[v]) + c0) * static_cast<int>(sizeof(TW));
+        if (!on[v])
+            for (int r = 0; r < R; ++r) ring.clear((r * V + v) * ONE, ONE);
         w[v] = vec_of(1.f);
         dw[v] = vec_of(0.f);
-        if (on[v] && a.norm && s.weight) {
-            const int at = (a.norm == kQkNormToken ? h * D : 0) + c, up = at + (HALVES ? half : 4);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                w[v].f[e] = make_float2(weight_at(s.weight, a.w_dtype, at + 2 * e), weight_at(s.weight, a.w_dtype, at + 2 * e + 1));
-                w[v].f[e + 2] = make_float2(weight_at(s.weight, a.w_dtype, up + 2 * e), weight_at(s.weight, a.w_dtype, up + 2 * e + 1));
-            }
-        }
+        if (on[v] && a.norm) w[v] = load_any<SPLIT>(s.weight, (a.norm == kQkNormToken ? head[v] * D : 0) + c0, a.w_dtype, 1.f, gap);
     }
+    const RopeSide& sq = a.side[side_q];
+    const RopeSide& sk = a.side[1];
 
-    int lp = l0, left = n;
+    int lp = l0, left = n;  // token of the next row to copy, rows still to copy
     auto prefetch = [&]() {
-        if (left > 0) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (left <= 0) break;
             --left;
-            const bool last = ++lp == a.tokens;
-            if (last) lp = 0;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const RopeSide& q = a.side[0];
-                const RopeSide& k = a.side[1];
                 if (need_x) {
-                    if (on[v]) copy_in<TX, HALVES>(ring, v * ONE, px[v], half);
-                    px[v] += is_k[v] ? k.sx.l : q.sx.l;
-                    if (last) px[v] += is_k[v] ? k.sx.b - a.tokens * k.sx.l : q.sx.b - a.tokens * q.sx.l;
+                    if (on[v]) ring.copy<SPLIT>((r * V + v) * ONE, reinterpret_cast<const TX*>(px[v]), gap);
+                    px[v] += v < VQ ? sq.next_x : sk.next_x;
                 }
                 if (BWD) {
-                    if (on[v]) copy_in<TO, HALVES>(ring, v * ONE + UX, pd[v], half);
-                    pd[v] += is_k[v] ? k.sd.l : q.sd.l;
-                    if (last) pd[v] += is_k[v] ? k.sd.b - a.tokens * k.sd.l : q.sd.b - a.tokens * q.sd.l;
+                    if (on[v]) ring.copy<SPLIT>((r * V + v) * ONE + UX, reinterpret_cast<const TO*>(pd[v]), gap);
+                    pd[v] += v < VQ ? sq.next_d : sk.next_d;
                 }
             }
-            ring.filled();
+            if (++lp == a.tokens) {
+                lp = 0;
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    px[v] += v < VQ ? sq.wrap_x : sk.wrap_x;
+                    if (BWD) pd[v] += v < VQ ? sq.wrap_d : sk.wrap_d;
+                }
+            }
         }
+        ring.filled();
         async_commit();
     };
     for (int s = 0; s < a.stages - 1; ++s) prefetch();
 
-    // The table of the row whose batch and token are (tb, tl), in half `which` of the team's table; its
-    // grid place (gt, gh, gw) moves along with it.
-    const long long start = a.first + l0;
-    const int hw = a.positions ? 1 : a.H * a.W, gt0 = static_cast<int>(a.first / hw), g0 = static_cast<int>(a.first % hw);
-    int tb = b0, tl = l0, gt = static_cast<int>(start / hw), gh = 0, gw = 0;
-    if (!a.positions && a.rotate) gh = static_cast<int>(start % hw) / a.W, gw = static_cast<int>(start % hw) % a.W;
-    auto fill = [&](int which) {
-        float* cs = table + which * 2 * pairs;
-        for (int j = t; j < pairs; j += team_size) {
-            const int ax = axis[j];
-            const int p = a.positions ? a.positions[tb * a.positions_b + tl * 3ll + ax] : ax == 0 ? gt : ax == 1 ? gh : gw;
-            const double turn = static_cast<double>(p + a.offset[ax]) * turns[j];
-            float sn, c;
-            sincospif(2.0f * static_cast<float>(turn - rint(turn)), &sn, &c);
+    // Tables of a step's tokens (`count` of them from token tl of sample tb on), in half `which` of the team's
+    // tables.
+    int tb = b0, tl = l0;
+    auto fill = [&](int which, int count) {
+        for (int i = t; i < R * pairs; i += team_size) {
+            const int r = R > 1 && i >= pairs ? 1 : 0, j = i - r * pairs, ax = axis[j];
+            if (r >= count) break;
+            const bool over = tl + r >= a.tokens;  // the next sample's first token
+            const unsigned token = over ? 0 : tl + r;
+            int p;
+            if (a.positions) {
+                p = a.positions[(over ? tb + 1 : tb) * a.positions_b + token * 3ll + ax];
+            } else {
+                const unsigned place = a.first + token, y = place / a.W, z = y / a.H;
+                p = ax == 0 ? z : ax == 1 ? y - z * a.H : place - y * a.W;
+            }
+            const unsigned long long turn = static_cast<unsigned long long>(p + a.offset[ax]) * turns[j];
+            float sn, c;  // of the signed fraction in half turns
+            sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f, &sn, &c);
+            float* cs = table + (which * R + r) * 2 * pairs;
             cs[j] = c;
             cs[pairs + j] = BWD ? -sn : sn;  // the gradient turns back
         }
-        if (++tl == a.tokens) {
-            tl = 0, ++tb;
-            if (!a.positions) gt = gt0, gh = g0 / a.W, gw = g0 % a.W;
-        } else if (++gw == a.W) {
-            gw = 0;
-            if (++gh == a.H) gh = 0, ++gt;
-        }
+        for (tl += R; tl >= a.tokens; tl -= a.tokens) ++tb;
     };
     if (a.rotate) {
-        if (n > 0) fill(0);
+        if (n > 0) fill(0, n);
         team.sync();
     }
 
     const float inv_head = 1.0f / D;
-    const float inv_q = 1.0f / (static_cast<float>(D) * q_heads);
+    const float inv_q = 1.0f / (static_cast<float>(D) * a.side[side_q].heads);
     const float inv_k = 1.0f / (static_cast<float>(D) * max(1, a.side[1].heads));
     const bool has_pairs = lane * 8 < D;
-    int l = l0;
-    for (int i = 0; i < iters; ++i) {
+    int l = l0, which = 0;
+    for (int i = 0; i < longest; i += R) {
         prefetch();
-        const bool row = WIDE || i < n;
-        float2 c[2] = {both(1.f), both(1.f)}, sn[2] = {both(0.f), both(0.f)};
+        float2 c[R][2], sn[R][2];
         if (a.rotate) {
-            if (has_pairs) {
-                const float4* cs = reinterpret_cast<const float4*>(table + (i & 1) * 2 * pairs);
-                const float4 u = cs[lane], z = cs[pairs / 4 + lane];
-                c[0] = make_float2(u.x, u.y), c[1] = make_float2(u.z, u.w);
-                sn[0] = make_float2(z.x, z.y), sn[1] = make_float2(z.z, z.w);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                c[r][0] = c[r][1] = sn[r][0] = sn[r][1] = both(0.f);
+                if (has_pairs) {
+                    const float4* cs = reinterpret_cast<const float4*>(table + (which * R + r) * 2 * pairs);
+                    const float4 u = cs[lane], z = cs[pairs / 4 + lane];
+                    c[r][0] = make_float2(u.x, u.y), c[r][1] = make_float2(u.z, u.w);
+                    sn[r][0] = make_float2(z.x, z.y), sn[r][1] = make_float2(z.z, z.w);
+                }
             }
-            if (i + 1 < n) fill((i + 1) & 1);
-            // every thread has read this row's table and sees the next one after a barrier of the team
+            which ^= 1;
+            if (i + R < n) fill(which, n - i - R);
+            // every thread has read this step's tables and sees the next ones after a barrier of the team
             if (!WIDE || a.norm != kQkNormToken) team.sync();
         }
         ring_wait(a.stages);
 
-        Vec x[V], g[V];
+        Vec x[R][V], g[R][V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (need_x) x[v] = ring.read<TX>(v * ONE);
-            if (BWD) {
-                g[v] = ring.read<TO>(v * ONE + UX);
-                if (a.rotate) rotate<HALVES>(g[v], c, sn);
-            }
-        }
-        ring.done();
-        // per vector: r, and r^2 mean(g w x) of the norm it belongs to
-        float r[V], gx[V];
-        if (a.norm) {
-            float qq[V], z[V];
+        for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                float2 s1 = mul2(x[v].f[0], x[v].f[0]), s2 = both(0.f);
-#pragma unroll
-                for (int e = 1; e < 4; ++e) s1 = fma2(x[v].f[e], x[v].f[e], s1);
-                if (BWD)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s2 = fma2(mul2(g[v].f[e], w[v].f[e]), x[v].f[e], s2);
-                qq[v] = fold(s1);
-                z[v] = BWD ? fold(s2) : 0.f;
+                if (need_x) x[r][v] = ring.read<TX>((r * V + v) * ONE);
+                if (BWD) {
+                    g[r][v] = ring.read<TO>((r * V + v) * ONE + UX);
+                    if (a.rotate) rotate<SPLIT>(g[r][v], c[r], sn[r]);
+                }
             }
+        ring.done();
+        // per vector: rd = 1 / rms, and rd^2 mean(g w x) of the norm it belongs to
+        float rd[R][V], gx[R][V];
+        if (a.norm) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const Vec& xv = x[r][v];
+                    float2 s1 = mul2(xv.f[0], xv.f[0]), s2 = both(0.f);
+#pragma unroll
+                    for (int e = 1; e < 4; ++e) s1 = fma2(xv.f[e], xv.f[e], s1);
+                    if (BWD)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s2 = fma2(mul2(g[r][v].f[e], w[v].f[e]), xv.f[e], s2);
+                    rd[r][v] = fold(s1);
+                    gx[r][v] = BWD ? fold(s2) : 0.f;
+                }
             if (a.norm == kQkNormHead) {
+                for (int o = G >> 1; o > 0; o >>= 1)
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    for (int o = G >> 1; o > 0; o >>= 1) {
-                        qq[v] += Team<WIDE>::swap(qq[v], o);
-                        if (BWD) z[v] += Team<WIDE>::swap(z[v], o);
+                    for (int r = 0; r < R; ++r)
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            rd[r][v] += Team<WIDE>::swap(rd[r][v], o);
+                            if (BWD) gx[r][v] += Team<WIDE>::swap(gx[r][v], o);
+                        }
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        rd[r][v] = rsqrtf(rd[r][v] * inv_head + a.eps);
+                        gx[r][v] *= inv_head * rd[r][v] * rd[r][v];
                     }
-                    r[v] = rsqrtf(qq[v] * inv_head + a.eps);
-                    if (BWD) gx[v] = z[v] * inv_head * r[v] * r[v];
-                }
             } else {
-                float q[BWD ? 4 : 2] = {};
+                constexpr int S = VK ? 2 : 1, N = S * (BWD ? 2 : 1);  // sums of a row: x^2 a side, then g w x
+                float sums[N * R];
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    q[0] += is_k[v] ? 0.f : qq[v];
-                    q[1] += is_k[v] ? qq[v] : 0.f;
-                    if constexpr (BWD) {
-                        q[2] += is_k[v] ? 0.f : z[v];
-                        q[3] += is_k[v] ? z[v] : 0.f;
+                for (int r = 0; r < R; ++r) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) sums[N * r + i] = 0.f;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const int side = v < VQ ? 0 : S - 1;
+                        sums[N * r + side] += rd[r][v];
+                        if constexpr (BWD) sums[N * r + S + side] += gx[r][v];
                     }
                 }
-                team.sum(q);
-                const float rq = rsqrtf(q[0] * inv_q + a.eps), rk = rsqrtf(q[1] * inv_k + a.eps);
+                team.sum(sums);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    r[v] = is_k[v] ? rk : rq;
-                    if constexpr (BWD) gx[v] = is_k[v] ? q[3] * inv_k * rk * rk : q[2] * inv_q * rq * rq;
-                }
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const int side = v < VQ ? 0 : S - 1;
+                        const float inv = side == 0 ? inv_q : inv_k;
+                        rd[r][v] = rsqrtf(sums[N * r + side] * inv + a.eps);
+                        if constexpr (BWD) gx[r][v] = sums[N * r + S + side] * inv * rd[r][v] * rd[r][v];
+                    }
             }
         }
-        const bool last = l + 1 == a.tokens;
-        l = last ? 0 : l + 1;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (!BWD) {
-                if (a.norm)
+        for (int r = 0; r < R; ++r) {
+            const bool row = i + r < n;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[v].f[e] = mul2(x[v].f[e], mul2(w[v].f[e], both(r[v])));
-                if (a.rotate) rotate<HALVES>(x[v], c, sn);
-                if (row && on[v]) store_out<TW, HALVES>(po[v], half, x[v]);
-            } else {
-                if (a.norm) {
-                    const float2 rr = both(r[v]), mg = both(-gx[v]);
+            for (int v = 0; v < V; ++v) {
+                TW* out = reinterpret_cast<TW*>(po[v]);
+                po[v] += v < VQ ? sq.next_o : sk.next_o;
+                if (!BWD) {
+                    if (a.norm)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (row) dw[v].f[e] = fma2(g[v].f[e], mul2(x[v].f[e], rr), dw[v].f[e]);
-                        g[v].f[e] = mul2(rr, fma2(x[v].f[e], mg, mul2(g[v].f[e], w[v].f[e])));
+                        for (int e = 0; e < 4; ++e)
+                            x[r][v].f[e] = mul2(x[r][v].f[e], mul2(w[v].f[e], both(rd[r][v])));
+                    if (a.rotate) rotate<SPLIT>(x[r][v], c[r], sn[r]);
+                    if (row && on[v]) store_vec<TW, SPLIT>(out, x[r][v], gap);
+                } else {
+                    if (a.norm) {
+                        const float2 rr = both(rd[r][v]), mg = both(-gx[r][v]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (row) dw[v].f[e] = fma2(g[r][v].f[e], mul2(x[r][v].f[e], rr), dw[v].f[e]);
+                            g[r][v].f[e] = mul2(rr, fma2(x[r][v].f[e], mg, mul2(g[r][v].f[e], w[v].f[e])));
+                        }
                     }
+                    if (row && on[v]) store_vec<TW, SPLIT>(out, g[r][v], gap);
                 }
-                if (row && on[v]) store_out<TW, HALVES>(po[v], half, g[v]);
             }
-            const Strides& sq = a.side[0].so;
-            const Strides& sk = a.side[1].so;
-            po[v] += is_k[v] ? sk.l : sq.l;
-            if (last) po[v] += is_k[v] ? sk.b - a.tokens * sk.l : sq.b - a.tokens * sq.l;
+            if (++l == a.tokens) {
+                l = 0;
+#pragma unroll
+                for (int v = 0; v < V; ++v) po[v] += v < VQ ? sq.wrap_o : sk.wrap_o;
+            }
         }
     }
 
     if (!BWD || !a.part) return;
+    const int sides = a.side[1].heads > 0 ? 2 : 1;
     if (a.norm == kQkNormToken) {
-        float* part = a.part + static_cast<long long>(worker) * heads * D;
+        float* sums = a.part + static_cast<long long>(worker) * (a.side[0].heads + a.side[1].heads) * D + c0;
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (on[v]) store_out<float, HALVES>(part + (t + v * team_size) / G * D + lane * (HALVES ? 4 : 8), half, dw[v]);
+            if (on[v])
+                store_vec<float, SPLIT>(sums + (head[v] + ((v < VQ ? side_q : 1) ? a.side[0].heads : 0)) * D, dw[v], gap);
         return;
     }
-    // one weight for all heads of a side: joined over the heads in order, through the ring's memory
+    // one weight for all heads of a side: joined over the block's heads in order, through the ring's memory
     async_wait<0>();
     __syncthreads();
     Vec* sums = reinterpret_cast<Vec*>(shared);
 #pragma unroll
     for (int v = 0; v < V; ++v) sums[v * blockDim.x + threadIdx.x] = dw[v];
     __syncthreads();
-    const int sides = heads > q_heads ? 2 : 1;
     for (int j = t; j < sides * G; j += team_size) {
         const int side = j / G, place = j % G;
         if (place * 8 >= D) continue;
         Vec d = vec_of(0.f);
-        for (int h = side ? q_heads : 0; h < (side ? heads : q_heads); ++h) {
-            const int slot = h * G + place, v = slot / team_size, at = in_block * team_size + slot % team_size;
-            const Vec u = sums[v * blockDim.x + at];
+        // none where the other blocks have this side
+        const int count = a.split_sides && side != part ? 0 : min(a.side[side].heads - piece * a.part_heads[side], a.part_heads[side]);
+        for (int h = 0; h < count; ++h) {
+            const int slot = h * G + place, v = slot / team_size + (side != side_q ? VQ : 0);
+            const Vec u = sums[v * blockDim.x + in_block * team_size + slot % team_size];
 #pragma unroll
             for (int e = 0; e < 4; ++e) d.f[e] = add2(d.f[e], u.f[e]);
         }
-        store_out<float, HALVES>(a.part + (static_cast<long long>(worker) * sides + side) * D + place * (HALVES ? 4 : 8),
-                                 half, d);
+        store_vec<float, SPLIT>(a.part + ((static_cast<long long>(worker) * a.parts + part) * sides + side) * D + place * (SPLIT ? 4 : 8), d, gap);
     }
 }
 
 // The weights' gradients: the workers' sums joined in a fixed order, 32 columns a block.
-constexpr int kFinalWarps = 16;
+constexpr int kFinalWarps = 32;
 __global__ void __launch_bounds__(32 * kFinalWarps) qk_rope_final_kernel(const float* part, int workers, int columns,
                                                                          int q_columns, float* dwq, float* dwk) {
     __shared__ float red[kFinalWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float sum = 0.f;
     if (c < columns)
+#pragma unroll 4
         for (int w = warp; w < workers; w += kFinalWarps) sum += part[static_cast<long long>(w) * columns + c];
     red[warp][lane] = sum;
     __syncthreads();
@@ -356,16 +367,27 @@ int group_of(int head_dim) {
     return g;
 }
 
-// Blocks that a processor holds at once, from the registers the kernels need.
-int blocks_per_sm(const RowPlan& p, bool backward) { return std::max(1, (p.V == 1 ? 1024 : 640) / p.threads); }
+// Registers of a thread with V vectors (block-wide teams, several teams a block), and the blocks that an SM
+// then holds at once.
+int blocks_per_sm(const RowPlan& p, bool backward) {
+    const int wide[2][4] = {{0, 80, 96, 128}, {0, 96, 120, 168}}, narrow[2][3] = {{0, 80, 120}, {0, 120, 128}};
+    return std::max(1, 65536 / ((p.team <= 32 ? narrow[backward][p.V] : wide[backward][p.V]) * p.threads));
+}
 
-template <typename TX, typename TO, int V, bool HALVES, bool BWD, bool WIDE>
+template <typename TX, typename TO, int VQ, int VK, bool HALVES, bool BWD, bool WIDE>
 cudaError_t launch(QkRopeArgs a, const RowPlan& p, cudaStream_t st) {
-    const size_t stage = size_t(16) * V * (kUnits<TX> + (BWD ? kUnits<TO> : 0)) * p.threads;
+    for (RopeSide& s : a.side) {
+        const long long x = sizeof(TX), d = sizeof(TO), o = BWD ? sizeof(TX) : sizeof(TO);
+        s.next_x = s.sx.l * x, s.wrap_x = (s.sx.b - a.tokens * s.sx.l) * x;
+        s.next_d = s.sd.l * d, s.wrap_d = (s.sd.b - a.tokens * s.sd.l) * d;
+        s.next_o = s.so.l * o, s.wrap_o = (s.so.b - a.tokens * s.so.l) * o;
+    }
+    constexpr int R = kRows<VQ + VK, BWD>;
+    const size_t stage = size_t(16) * R * (VQ + VK) * (kUnits<TX> + (BWD ? kUnits<TO> : 0)) * p.threads;
     const int per_sm = blocks_per_sm(p, BWD);
-    a.stages = ring_stages(stage, per_sm, kRingBytes / per_sm);
-    const size_t smem = a.stages * stage + size_t(p.threads / p.team) * 2 * a.head_dim * sizeof(float);
-    const auto kernel = qk_rope_kernel<TX, TO, V, HALVES, BWD, WIDE>;
+    a.stages = ring_stages(stage, per_sm, kRingBytes / per_sm, (a.rows + a.workers - 1) / a.workers, R);
+    const size_t smem = a.stages * stage + size_t(p.threads / p.team) * 2 * R * a.head_dim * sizeof(float);
+    const auto kernel = qk_rope_kernel<TX, TO, VQ, VK, HALVES, BWD, WIDE>;
     if (smem > 40 * 1024) {  // 48 KB without opting in, less the static part
         const cudaError_t e =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -374,54 +396,103 @@ cudaError_t launch(QkRopeArgs a, const RowPlan& p, cudaStream_t st) {
     kernel<<<p.blocks, p.threads, smem, st>>>(a);
     return cudaGetLastError();
 }
-template <typename TX, typename TO, int V, bool WIDE>
+template <typename TX, typename TO, int VQ, int VK, bool WIDE>
 cudaError_t launch_dir(const QkRopeArgs& a, const RowPlan& p, bool backward, cudaStream_t st) {
     if (a.halves)
-        return backward ? launch<TX, TO, V, true, true, WIDE>(a, p, st) : launch<TX, TO, V, true, false, WIDE>(a, p, st);
-    return backward ? launch<TX, TO, V, false, true, WIDE>(a, p, st) : launch<TX, TO, V, false, false, WIDE>(a, p, st);
+        return backward ? launch<TX, TO, VQ, VK, true, true, WIDE>(a, p, st) : launch<TX, TO, VQ, VK, true, false, WIDE>(a, p, st);
+    return backward ? launch<TX, TO, VQ, VK, false, true, WIDE>(a, p, st) : launch<TX, TO, VQ, VK, false, false, WIDE>(a, p, st);
 }
 template <typename TX, typename TO>
-cudaError_t launch_types(const QkRopeArgs& a, const RowPlan& p, bool backward, cudaStream_t st) {
-    return p.team <= 32 ? launch_dir<TX, TO, 1, false>(a, p, backward, st)
-           : p.V == 1   ? launch_dir<TX, TO, 1, true>(a, p, backward, st)
-           : p.V == 2   ? launch_dir<TX, TO, 2, true>(a, p, backward, st)
-                        : launch_dir<TX, TO, 4, true>(a, p, backward, st);
+cudaError_t launch_types(const QkRopeArgs& a, const RowPlan& p, int VQ, bool backward, cudaStream_t st) {
+    const bool k = p.V > VQ;
+    if (p.team <= 32)
+        return k ? launch_dir<TX, TO, 1, 1, false>(a, p, backward, st) : launch_dir<TX, TO, 1, 0, false>(a, p, backward, st);
+    if (VQ == 1)
+        return k ? launch_dir<TX, TO, 1, 1, true>(a, p, backward, st) : launch_dir<TX, TO, 1, 0, true>(a, p, backward, st);
+    return k ? launch_dir<TX, TO, 2, 1, true>(a, p, backward, st) : launch_dir<TX, TO, 2, 0, true>(a, p, backward, st);
+}
+
+// A block takes all heads of a token, or, where those are too many for it, a part of q's and of k's (no norm,
+// or one per head), or q's or k's (a norm over the heads: they never share one).
+struct RopePlan {
+    RowPlan rows;
+    int VQ, VK, split_sides, part_heads[2];
+};
+
+RopePlan plan_of(long long rows, int head_dim, int q_heads, int k_heads, int norm, bool backward) {
+    RopePlan best;
+    const int G = group_of(head_dim);
+    long long least = -1;
+    // parts of the heads, or sides apart (parts 0); vectors a thread of q and of k, or of the side
+    for (int parts = 0; parts <= 16; ++parts) {
+        if ((norm == kQkNormToken && parts > 1) || (parts == 0 && !k_heads)) continue;
+        const int hq = parts ? (q_heads + parts - 1) / parts : std::max(q_heads, k_heads);
+        const int hk = parts ? (k_heads + parts - 1) / parts : 0;
+        for (int vq = 1; vq <= 2; ++vq) {
+            RopePlan c;
+            RowPlan& p = c.rows;
+            c.VQ = vq;
+            c.VK = hk ? 1 : 0;
+            row_team(std::max((hq * G + vq - 1) / vq, hk * G), 1, &p);
+            p.V = c.VQ + c.VK;
+            if (p.team % G != 0 || p.threads > rope_threads(p.V, backward) || (p.team <= 32 && vq > 1)) continue;
+            // Thread-steps of a row: a step costs about as much as one vector besides its vectors, and an
+            // entry of the table as much as another; registers that a thread needs are threads that the SM
+            // lacks.  Sides apart cost both blocks the table, and leave threads idle where they are unequal.
+            const int registers[2][4] = {{0, 80, 96, 128}, {0, 96, 120, 168}};
+            const int steps = backward && p.V > 1 ? 2 : 1;
+            const int shares = parts ? parts : 2 * std::min(q_heads, k_heads) < std::max(q_heads, k_heads) ? 3 : 2;
+            const long long cost = static_cast<long long>((2 * p.V + steps) * p.team + head_dim) *
+                                   registers[backward][p.V] * shares;
+            if (least >= 0 && cost >= least) continue;
+            least = cost;
+            c.split_sides = parts == 0;
+            c.part_heads[0] = hq;
+            c.part_heads[1] = parts ? hk : hq;
+            p.parts = parts ? parts : 2;
+            best = c;
+        }
+    }
+    RowPlan& p = best.rows;
+    const int parts = p.parts;
+    row_workers(rows, std::max(1, kSMs * blocks_per_sm(p, backward) / parts), &p);
+    p.parts = parts;
+    p.blocks *= parts;
+    return best;
 }
 
 }  // namespace
 
-RowPlan qk_rope_plan(long long rows, int head_dim, int heads, bool backward) {
-    RowPlan p;
-    const int slots = heads * group_of(head_dim);
-    int V = 1;
-    while (V < 4 && (slots + V - 1) / V > rope_threads(V)) V *= 2;
-    row_team(slots, V, &p);
-    row_workers(rows, kSMs * blocks_per_sm(p, backward), &p);
-    return p;
+RowPlan qk_rope_plan(long long rows, int head_dim, int q_heads, int k_heads, int norm, bool backward) {
+    return plan_of(rows, head_dim, q_heads, k_heads, norm, backward).rows;
 }
 
 cudaError_t launch_qk_rope(const QkRopeArgs& args, bool backward, cudaStream_t st) {
     QkRopeArgs a = args;
-    const int heads = a.side[0].heads + a.side[1].heads;
-    const RowPlan p = qk_rope_plan(a.rows, a.head_dim, heads, backward);
+    const RopePlan plan = plan_of(a.rows, a.head_dim, a.side[0].heads, a.side[1].heads, a.norm, backward);
+    const RowPlan& p = plan.rows;
+    a.parts = p.parts;
+    a.split_sides = plan.split_sides;
+    a.part_heads[0] = plan.part_heads[0];
+    a.part_heads[1] = plan.part_heads[1];
     a.group = group_of(a.head_dim);
     a.team = p.team;
     a.workers = p.workers;
     cudaError_t e;
     if (a.x_dtype == kF32)
-        e = launch_types<float, float>(a, p, backward, st);
+        e = launch_types<float, float>(a, p, plan.VQ, backward, st);
     else if (a.x_dtype == kBf16)
-        e = a.out_dtype == kF32 ? launch_types<__nv_bfloat16, float>(a, p, backward, st)
-                                : launch_types<__nv_bfloat16, __nv_bfloat16>(a, p, backward, st);
+        e = a.out_dtype == kF32 ? launch_types<__nv_bfloat16, float>(a, p, plan.VQ, backward, st)
+                                : launch_types<__nv_bfloat16, __nv_bfloat16>(a, p, plan.VQ, backward, st);
     else
-        e = a.out_dtype == kF32 ? launch_types<__half, float>(a, p, backward, st)
-                                : launch_types<__half, __half>(a, p, backward, st);
+        e = a.out_dtype == kF32 ? launch_types<__half, float>(a, p, plan.VQ, backward, st)
+                                : launch_types<__half, __half>(a, p, plan.VQ, backward, st);
     if (e != cudaSuccess || !backward || !a.part) return e;
     const bool per_head = a.norm == kQkNormToken;  // a weight for each head
     const int q_columns = a.head_dim * (per_head ? a.side[0].heads : 1);
     const int k_columns = a.head_dim * (per_head ? a.side[1].heads : a.side[1].heads > 0);
     const int columns = q_columns + k_columns;
-    qk_rope_final_kernel<<<(columns + 31) / 32, 32 * kFinalWarps, 0, st>>>(a.part, p.workers, columns, q_columns,
+    qk_rope_final_kernel<<<(columns + 31) / 32, 32 * kFinalWarps, 0, st>>>(a.part, per_head ? p.workers : p.workers * p.parts, columns, q_columns,
                                                                            a.side[0].dweight, a.side[1].dweight);
     return cudaGetLastError();
 }

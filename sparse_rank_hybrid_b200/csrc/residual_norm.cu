@@ -36,21 +36,14 @@ constexpr size_t kRingBytes = 200 * 1024;  // dynamic shared memory of an SM's b
 constexpr int fwd_threads(int V) { return V == 1 ? 1024 : 640; }
 constexpr int bwd_threads(int V) { return V == 1 ? 640 : 512; }
 
-// A pointer that walks a worker's rows through a [B][L][C] tensor with free batch and token strides.
-template <typename T>
-struct RowWalk {
-    T* p;
-    __device__ RowWalk(const RowTensor& t, int b, int l, int column)
-        : p(static_cast<T*>(t.p) + b * t.b + l * t.l + column) {}
-    __device__ __forceinline__ void next(const RowTensor& t) { p += t.l; }
-    __device__ __forceinline__ void wrap(const RowTensor& t, int tokens) { p += t.b - tokens * t.l; }
-};
-
 // Brings a modulation row towards the SM before the row that needs it.
-__device__ __forceinline__ void prefetch_mod(const ModTensor& m, int dtype, int b, int f, int column) {
-    if (m.p)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(m.p) +
-                                                      (b * m.b + f * m.f + column) * (dtype == kF32 ? 4 : 2)));
+template <bool SPLIT>
+__device__ __forceinline__ void prefetch_mod(const ModTensor& m, int dtype, int b, int f, int column, int gap) {
+    if (!m.p) return;
+    const int size = dtype == kF32 ? 4 : 2;
+    const char* p = static_cast<const char*>(m.p) + (b * m.b + f * m.f + column) * size;
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+    if (SPLIT) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + gap * size));
 }
 
 // Mean and reciprocal standard deviation from sum(o) and sum(o^2).  One pass over the row loses a factor
@@ -63,55 +56,73 @@ __device__ __forceinline__ bool row_moments(float sum, float squares, float inv,
     return m * m > 4.f * var;
 }
 
-template <typename TS, typename TB, int V, bool HASY, bool WIDE>
+// The rows that a team of the grid works on, and where its threads stand in them.
+template <bool WIDE>
+struct Place {
+    int size, t, worker, n, longest, b0, l0;
+    __device__ Place(const ResidualNormArgs& a) {
+        size = WIDE ? blockDim.x : a.team;
+        t = WIDE ? threadIdx.x : threadIdx.x % a.team;
+        worker = WIDE ? blockIdx.x : blockIdx.x * (blockDim.x / a.team) + threadIdx.x / a.team;
+        const long long r0 = worker_lo(a.rows, a.workers, worker), r1 = worker_lo(a.rows, a.workers, worker + 1);
+        n = static_cast<int>(r1 - r0);
+        // teams of one warp take part in each other's shuffles, so they all loop as long as the longest
+        longest = WIDE ? n : static_cast<int>((a.rows + a.workers - 1) / a.workers);
+        b0 = static_cast<int>(r0 / a.tokens);
+        l0 = static_cast<int>(r0 % a.tokens);
+    }
+};
+
+// Y: 0 without y, 1 with it, 2 with its own norm.  A block-wide team takes ROWS rows a step while they share a
+// modulation row: what a step costs besides its vectors (the loop, the ring, the barrier and the sums'
+// exchanges) is shared by them, and the coefficients in registers serve both.
+template <typename TS, typename TB, int V, int Y, bool WIDE, int ROWS>
 __global__ void __launch_bounds__(WIDE ? fwd_threads(V) : 128) residual_norm_fwd_kernel(const __grid_constant__ ResidualNormArgs a) {
-    constexpr int UX = kUnits<TS>, UY = HASY ? kUnits<TB> : 0, U = V * (UX + UY);
+    constexpr bool SPLIT = sizeof(TS) == 4;
+    constexpr int UX = kUnits<TS>, ONE = UX + (Y ? kUnits<TB> : 0), U = ROWS * V * ONE;
     extern __shared__ uint4 shared[];
     __shared__ __align__(16) float scratch[kTeamScratch];
-    const int team_size = WIDE ? blockDim.x : a.team;
-    Team<WIDE> team(team_size, scratch);
-    const int t = WIDE ? threadIdx.x : threadIdx.x % a.team;
-    const int worker = WIDE ? blockIdx.x : blockIdx.x * (blockDim.x / a.team) + threadIdx.x / a.team;
-    const long long r0 = worker_lo(a.rows, a.workers, worker), r1 = worker_lo(a.rows, a.workers, worker + 1);
-    const int n = static_cast<int>(r1 - r0);
-    // teams of one warp take part in each other's shuffles, so they all loop as long as the longest
-    const int iters = WIDE ? n : static_cast<int>((a.rows + a.workers - 1) / a.workers);
-    const int b0 = static_cast<int>(r0 / a.tokens), l0 = static_cast<int>(r0 % a.tokens), c0 = t * 8;
-    const int step = team_size * 8;  // channels between a thread's vectors
+    const Place<WIDE> at(a);
+    Team<WIDE> team(at.size, scratch);
+    // first channel, channels between a thread's vectors and between the halves of one
+    const int c0 = at.t * (SPLIT ? 4 : 8), step = at.size * (SPLIT ? 4 : 8), gap = SPLIT ? a.channels / 2 : 4;
     const float inv = 1.0f / a.channels;
-    const bool layer = a.norm == kNormLayer;
+    const bool layer = a.norm == kNormLayer, scaled = a.rs != 1.f;
 
     Ring ring(shared_address(shared), a.stages, U);
     bool on[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        on[v] = c0 + v * step < a.channels;
-        if (!on[v]) ring.clear(v * (UX + UY), UX + UY);
+        on[v] = at.t + v * at.size < a.channels / 8;
+        if (!on[v])
+            for (int r = 0; r < ROWS; ++r) ring.clear((r * V + v) * ONE, ONE);
     }
-    RowWalk<const TS> px(a.x, b0, l0, c0);
-    RowWalk<const TB> py(HASY ? a.y : a.h, b0, l0, c0);
-    RowWalk<TS> pxo(HASY ? a.x_out : a.x, b0, l0, c0);
-    RowWalk<TB> ph(a.norm ? a.h : a.y, b0, l0, c0);
+    RowWalk<const TS> px(a.x, at.b0, at.l0, a.tokens);
+    RowWalk<const TB> py(a.y, at.b0, at.l0, a.tokens);
+    RowWalk<TS> pxo(a.x_out, at.b0, at.l0, a.tokens);
+    RowWalk<TB> ph(a.h, at.b0, at.l0, a.tokens);
 
-    int lp = l0, left = n;  // token of the next row to copy, rows still to copy
+    int lp = at.l0, left = at.n;  // token of the next row to copy, rows still to copy
     auto prefetch = [&]() {
-        if (left > 0) {
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            if (left <= 0) break;
             --left;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (!on[v]) continue;
-                ring.copy(v * (UX + UY), px.p + v * step);
-                if (HASY) ring.copy(v * (UX + UY) + UX, py.p + v * step);
+                ring.copy<SPLIT>((r * V + v) * ONE, px.at(0, c0 + v * step), gap);
+                if (Y) ring.copy<SPLIT>((r * V + v) * ONE + UX, py.at(0, c0 + v * step), gap);
             }
-            px.next(a.x);
-            if (HASY) py.next(a.y);
+            px.next();
+            if (Y) py.next();
             if (++lp == a.tokens) {
                 lp = 0;
-                px.wrap(a.x, a.tokens);
-                if (HASY) py.wrap(a.y, a.tokens);
+                px.wrap();
+                if (Y) py.wrap();
             }
-            ring.filled();
         }
+        ring.filled();
         async_commit();
     };
     for (int s = 0; s < a.stages - 1; ++s) prefetch();
@@ -119,184 +130,228 @@ __global__ void __launch_bounds__(WIDE ? fwd_threads(V) : 128) residual_norm_fwd
     Vec cg[V], ca[V], cb[V];  // gate wp, w (1 + scale), b (1 + scale) + shift
 #pragma unroll
     for (int v = 0; v < V; ++v) cg[v] = ca[v] = cb[v] = vec_of(0.f);
-    int b = b0, l = l0, f = l0 / a.per, group_left = 0;
-    for (int i = 0; i < iters; ++i) {
-        prefetch();
-        const bool row = WIDE || i < n;
-        if (row && group_left == 0) {  // another modulation row
-            group_left = a.per - (l - f * a.per);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = c0 + v * step;
-                if (!on[v]) continue;
-                if (HASY) {
-                    const Vec w = load_any(a.post_weight, c, a.w_dtype, 1.f);
-                    const Vec g = load_any(a.gate.p, b * a.gate.b + f * a.gate.f + c, a.mod_dtype, 1.f);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) cg[v].f[e] = mul2(w.f[e], g.f[e]);
-                }
-                if (a.norm) {
-                    const Vec sc = load_any(a.scale.p, b * a.scale.b + f * a.scale.f + c, a.mod_dtype, 0.f);
-                    const Vec sh = load_any(a.shift.p, b * a.shift.b + f * a.shift.f + c, a.mod_dtype, 0.f);
-                    const Vec w = load_any(a.weight, c, a.w_dtype, 1.f), bias = load_any(a.bias, c, a.w_dtype, 0.f);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 up = add2(sc.f[e], both(1.f));
-                        ca[v].f[e] = mul2(w.f[e], up);
-                        cb[v].f[e] = fma2(bias.f[e], up, sh.f[e]);
-                    }
-                }
-            }
-        }
-        if (row && group_left == 1 && i + 1 < n) {  // the next row's modulation
-            const bool wrap = l + 1 == a.tokens;
-            const int nb = wrap ? b + 1 : b, nf = wrap ? 0 : f + 1;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = c0 + v * step;
-                if (!on[v]) continue;
-                if (HASY) prefetch_mod(a.gate, a.mod_dtype, nb, nf, c);
-                prefetch_mod(a.scale, a.mod_dtype, nb, nf, c);
-                prefetch_mod(a.shift, a.mod_dtype, nb, nf, c);
-            }
-        }
-        ring_wait(a.stages);
-        Vec o[V], y[V];
+    int b = at.b0, l = at.l0, f = at.l0 / a.per, group_left = 0;
+
+    auto modulation = [&]() {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            o[v] = ring.read<TS>(v * (UX + UY));
-            if (HASY) y[v] = ring.read<TB>(v * (UX + UY) + UX);
+            const int c = c0 + v * step;
+            if (!on[v]) continue;
+            if (Y) {
+                const Vec w = load_any<SPLIT>(a.post_weight, c, a.w_dtype, 1.f, gap);
+                const Vec g = load_any<SPLIT>(a.gate.p, b * a.gate.b + f * a.gate.f + c, a.mod_dtype, 1.f, gap);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) cg[v].f[e] = mul2(w.f[e], g.f[e]);
+            }
+            if (a.norm) {
+                const Vec sc = load_any<SPLIT>(a.scale.p, b * a.scale.b + f * a.scale.f + c, a.mod_dtype, 0.f, gap);
+                const Vec sh = load_any<SPLIT>(a.shift.p, b * a.shift.b + f * a.shift.f + c, a.mod_dtype, 0.f, gap);
+                const Vec w = load_any<SPLIT>(a.weight, c, a.w_dtype, 1.f, gap);
+                const Vec bias = load_any<SPLIT>(a.bias, c, a.w_dtype, 0.f, gap);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 up = add2(sc.f[e], both(1.f));
+                    ca[v].f[e] = mul2(w.f[e], up);
+                    cb[v].f[e] = fma2(bias.f[e], up, sh.f[e]);
+                }
+            }
         }
-        ring.done();
-
-        if (HASY) {
-            if (a.post) {
-                float q[1] = {0.f};
+    };
+    // rows [r0, r0 + R) of the step
+    auto rows = [&](auto count, int r0, bool valid) {
+        constexpr int R = decltype(count)::value;
+        Vec o[R][V];
+        [[maybe_unused]] float ry[R];
+        if constexpr (Y == 2) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
                 float2 acc = both(0.f);
 #pragma unroll
-                for (int v = 0; v < V; ++v)
+                for (int v = 0; v < V; ++v) {
+                    const Vec y = ring.read<TB>(((r0 + r) * V + v) * ONE + UX);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc = fma2(y[v].f[e], y[v].f[e], acc);
-                q[0] = fold(acc);
-                team.sum(q);
-                const float2 ry = both(rsqrtf(q[0] * inv + a.post_eps));
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[v].f[e] = mul2(y[v].f[e], ry);
+                    for (int e = 0; e < 4; ++e) acc = fma2(y.f[e], y.f[e], acc);
+                }
+                ry[r] = fold(acc);
             }
-            const float2 rs = both(a.rs);
+            team.sum(ry);
+#pragma unroll
+            for (int r = 0; r < R; ++r) ry[r] = rsqrtf(ry[r] * inv + a.post_eps);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
+                o[r][v] = ring.read<TS>(((r0 + r) * V + v) * ONE);
+                if constexpr (Y != 0) {
+                    Vec y = ring.read<TB>(((r0 + r) * V + v) * ONE + UX);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[v].f[e] = fma2(cg[v].f[e], y[v].f[e], mul2(rs, o[v].f[e]));
-                if (row && on[v]) store_vec(pxo.p + v * step, o[v]);
+                    for (int e = 0; e < 4; ++e) {
+                        if (Y == 2) y.f[e] = mul2(y.f[e], both(ry[r]));
+                        if (scaled) o[r][v].f[e] = mul2(o[r][v].f[e], both(a.rs));
+                        o[r][v].f[e] = fma2(cg[v].f[e], y.f[e], o[r][v].f[e]);
+                    }
+                    if (valid && on[v]) store_vec<TS, SPLIT>(pxo.at(r, c0 + v * step), o[r][v], gap);
+                }
             }
-        }
-        if (a.norm) {
+        if (!a.norm) return;
+        float q[2 * R], m[R], rd[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
             float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    s1 = add2(s1, o[v].f[e]);
-                    s2 = fma2(o[v].f[e], o[v].f[e], s2);
+                    s1 = add2(s1, o[r][v].f[e]);
+                    s2 = fma2(o[r][v].f[e], o[r][v].f[e], s2);
                 }
-            float q[2] = {fold(s1), fold(s2)}, m, r;
-            team.sum(q);
-            const bool centre = row_moments(q[0], q[1], inv, a.eps, layer, m, r);
-            if (WIDE ? centre : __any_sync(0xffffffffu, centre)) {  // every team of a warp takes part in the sum
-                float c[1] = {0.f};
+            q[2 * r] = fold(s1), q[2 * r + 1] = fold(s2);
+        }
+        team.sum(q);
+        bool any = false, centre[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            centre[r] = row_moments(q[2 * r], q[2 * r + 1], inv, a.eps, layer, m[r], rd[r]);
+            any |= centre[r];
+        }
+        if (WIDE ? any : __any_sync(0xffffffffu, any)) {  // every team of a warp takes part in the sum
+            float c[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                c[r] = 0.f;
 #pragma unroll
                 for (int v = 0; v < V; ++v)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float2 d = add2(o[v].f[e], both(-m));
-                        if (on[v]) c[0] += fold(mul2(d, d));
+                        const float2 d = add2(o[r][v].f[e], both(-m[r]));
+                        if (on[v]) c[r] += fold(mul2(d, d));
                     }
-                team.sum(c);
-                if (centre) r = rsqrtf(c[0] * inv + a.eps);
             }
-            const float2 rr = both(r), mr = both(-m * r);
+            team.sum(c);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (centre[r]) rd[r] = rsqrtf(c[r] * inv + a.eps);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
+                const float2 rr = both(rd[r]), mr = both(-m[r] * rd[r]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[v].f[e] = fma2(fma2(o[v].f[e], rr, mr), ca[v].f[e], cb[v].f[e]);
-                if (row && on[v]) store_vec(ph.p + v * step, o[v]);
+                for (int e = 0; e < 4; ++e) o[r][v].f[e] = fma2(fma2(o[r][v].f[e], rr, mr), ca[v].f[e], cb[v].f[e]);
+                if (valid && on[v]) store_vec<TB, SPLIT>(ph.at(r, c0 + v * step), o[r][v], gap);
             }
-        }
-        if (row) {
-            --group_left;
-            ++l;
-            if (HASY) pxo.next(a.x_out);
-            if (a.norm) ph.next(a.h);
-            if (group_left == 0) ++f;
+    };
+    // moves on by R rows, which end at a modulation row's end at the latest
+    auto advance = [&](int R) {
+        l += R;
+        group_left -= R;
+        if (Y) pxo.next(R);
+        ph.next(R);
+        if (group_left == 0) {
+            ++f;
             if (l == a.tokens) {
                 l = f = 0;
                 ++b;
-                if (HASY) pxo.wrap(a.x_out, a.tokens);
-                if (a.norm) ph.wrap(a.h, a.tokens);
+                if (Y) pxo.wrap();
+                ph.wrap();
             }
         }
+    };
+
+    for (int i = 0; i < at.longest; i += ROWS) {
+        prefetch();
+        ring_wait(a.stages);
+        const int rest = at.n - i;  // rows of this step and behind it
+        if (WIDE && ROWS > 1 && rest >= ROWS && group_left >= ROWS) {
+            rows(Count<ROWS>{}, 0, true);
+            advance(ROWS);
+        } else {
+#pragma unroll 1
+            for (int r = 0; r < ROWS; ++r) {
+                const bool valid = r < rest;
+                if (WIDE && !valid) break;
+                if (valid && group_left == 0) {
+                    modulation();
+                    group_left = a.per - (l - f * a.per);
+                }
+                if (valid && group_left == 1 && rest > r + 1) {  // the next row has another modulation row
+                    const bool wrap = l + 1 == a.tokens;
+                    const int nb = wrap ? b + 1 : b, nf = wrap ? 0 : f + 1;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const int c = c0 + v * step;
+                        if (!on[v]) continue;
+                        if (Y) prefetch_mod<SPLIT>(a.gate, a.mod_dtype, nb, nf, c, gap);
+                        prefetch_mod<SPLIT>(a.scale, a.mod_dtype, nb, nf, c, gap);
+                        prefetch_mod<SPLIT>(a.shift, a.mod_dtype, nb, nf, c, gap);
+                    }
+                }
+                rows(Count<1>{}, r, valid);
+                if (valid) advance(1);
+            }
+        }
+        ring.done();
     }
 }
 
-template <typename TS, typename TB, int V, bool HASY, bool WIDE>
+template <typename TS, typename TB, int V, int Y, bool WIDE, int ROWS>
 __global__ void __launch_bounds__(WIDE ? bwd_threads(V) : 128) residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a) {
+    constexpr bool SPLIT = sizeof(TS) == 4;
     constexpr int UX = kUnits<TS>, UB = kUnits<TB>;
-    constexpr int ONE = 2 * UX + (HASY ? 2 : 1) * UB, U = V * ONE;  // x, dx_out, dh and y of each vector
-    constexpr int DXO = UX, DH = 2 * UX, Y = 2 * UX + UB;
+    // x, dx_out, dh and y of each vector
+    constexpr int DXO = UX, DH = 2 * UX, YU = 2 * UX + UB, ONE = 2 * UX + (Y ? 2 : 1) * UB, U = ROWS * V * ONE;
     extern __shared__ uint4 shared[];
     __shared__ __align__(16) float scratch[kTeamScratch];
-    const int team_size = WIDE ? blockDim.x : a.team;
-    Team<WIDE> team(team_size, scratch);
-    const int t = WIDE ? threadIdx.x : threadIdx.x % a.team;
-    const int worker = WIDE ? blockIdx.x : blockIdx.x * (blockDim.x / a.team) + threadIdx.x / a.team;
-    const long long r0 = worker_lo(a.rows, a.workers, worker), r1 = worker_lo(a.rows, a.workers, worker + 1);
-    const int n = static_cast<int>(r1 - r0);
-    const int iters = WIDE ? n : static_cast<int>((a.rows + a.workers - 1) / a.workers);
-    const int b0 = static_cast<int>(r0 / a.tokens), l0 = static_cast<int>(r0 % a.tokens), c0 = t * 8;
-    const int step = team_size * 8;
+    const Place<WIDE> at(a);
+    Team<WIDE> team(at.size, scratch);
+    const int c0 = at.t * (SPLIT ? 4 : 8), step = at.size * (SPLIT ? 4 : 8), gap = SPLIT ? a.channels / 2 : 4;
     const float inv = 1.0f / a.channels;
     const bool layer = a.norm == kNormLayer, has_dxo = a.dx_out.p != nullptr, has_dh = a.norm != kNormNone;
+    const bool scaled = a.rs != 1.f;
 
     Ring ring(shared_address(shared), a.stages, U);
     bool on[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        on[v] = c0 + v * step < a.channels;
-        if (!on[v]) ring.clear(v * ONE, ONE);
+        on[v] = at.t + v * at.size < a.channels / 8;
+        if (!on[v])
+            for (int r = 0; r < ROWS; ++r) ring.clear((r * V + v) * ONE, ONE);
     }
-    RowWalk<const TS> px(a.x, b0, l0, c0), pdo(a.dx_out, b0, l0, c0);
-    RowWalk<const TB> py(a.y, b0, l0, c0), pdh(a.dh, b0, l0, c0);
-    RowWalk<TS> pdx(a.dx, b0, l0, c0);
-    RowWalk<TB> pdy(a.dy, b0, l0, c0);
+    RowWalk<const TS> px(a.x, at.b0, at.l0, a.tokens), pdo(a.dx_out, at.b0, at.l0, a.tokens);
+    RowWalk<const TB> py(a.y, at.b0, at.l0, a.tokens), pdh(a.dh, at.b0, at.l0, a.tokens);
+    RowWalk<TS> pdx(a.dx, at.b0, at.l0, a.tokens);
+    RowWalk<TB> pdy(a.dy, at.b0, at.l0, a.tokens);
 
-    int lp = l0, left = n;
+    int lp = at.l0, left = at.n;
     auto prefetch = [&]() {
-        if (left > 0) {
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            if (left <= 0) break;
             --left;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (!on[v]) continue;
-                ring.copy(v * ONE, px.p + v * step);
-                if (has_dxo) ring.copy(v * ONE + DXO, pdo.p + v * step);
-                if (has_dh) ring.copy(v * ONE + DH, pdh.p + v * step);
-                if (HASY) ring.copy(v * ONE + Y, py.p + v * step);
+                const int u = (r * V + v) * ONE;
+                ring.copy<SPLIT>(u, px.at(0, c0 + v * step), gap);
+                if (has_dxo) ring.copy<SPLIT>(u + DXO, pdo.at(0, c0 + v * step), gap);
+                if (has_dh) ring.copy<SPLIT>(u + DH, pdh.at(0, c0 + v * step), gap);
+                if (Y) ring.copy<SPLIT>(u + YU, py.at(0, c0 + v * step), gap);
             }
-            px.next(a.x);
-            pdo.next(a.dx_out);
-            pdh.next(a.dh);
-            if (HASY) py.next(a.y);
+            px.next();
+            pdo.next();
+            pdh.next();
+            if (Y) py.next();
             if (++lp == a.tokens) {
                 lp = 0;
-                px.wrap(a.x, a.tokens);
-                pdo.wrap(a.dx_out, a.tokens);
-                pdh.wrap(a.dh, a.tokens);
-                if (HASY) py.wrap(a.y, a.tokens);
+                px.wrap();
+                pdo.wrap();
+                pdh.wrap();
+                if (Y) py.wrap();
             }
-            ring.filled();
         }
+        ring.filled();
         async_commit();
     };
     for (int s = 0; s < a.stages - 1; ++s) prefetch();
@@ -307,279 +362,344 @@ __global__ void __launch_bounds__(WIDE ? bwd_threads(V) : 128) residual_norm_bwd
     for (int v = 0; v < V; ++v) cg[v] = ca[v] = p0[v] = p1[v] = pq[v] = vec_of(0.f);
     // Sums of the weights' gradients over all rows of the worker, added to at the end of each modulation
     // row: this thread's part of shared memory where it has room, else of the worker's slot in wpart.
-    float* wslot = a.wpart + static_cast<long long>(worker) * 3 * a.channels + c0;
+    // Element e of vector v of sum k is at k wk + v wv + e we (+ wg in the vector's second half).
+    float* wslot = a.wpart + static_cast<long long>(at.worker) * 3 * a.channels + c0;
     float* wsum = wslot;
-    int wk = a.channels, wv = step, we = 1;  // strides of the sum, the vector and the element
+    int wk = a.channels, wv = step, we = 1, wg = gap - 4;
     if (a.wsum_shared) {
         wsum = reinterpret_cast<float*>(shared) + static_cast<size_t>(a.stages) * U * 4 * blockDim.x + threadIdx.x;
-        we = blockDim.x, wv = 8 * we, wk = V * wv;
+        we = blockDim.x, wv = 8 * we, wk = V * wv, wg = 0;
     }
     if (a.wpart)
-        for (int v = 0; v < V && c0 + v * step < a.channels; ++v)
+        for (int v = 0; v < V && on[v]; ++v)
             for (int k = 0; k < 3; ++k)
-                for (int e = 0; e < 8; ++e) wsum[k * wk + v * wv + e * we] = 0.f;
+                for (int e = 0; e < 8; ++e) wsum[k * wk + v * wv + e * we + (e < 4 ? 0 : wg)] = 0.f;
+    auto add_weights = [&](int k, int v, int e, float2 d) {  // elements 2e, 2e + 1
+        float* w = wsum + k * wk + v * wv + 2 * e * we + (e < 2 ? 0 : wg);
+        w[0] += d.x;
+        w[we] += d.y;
+    };
 
-    int b = b0, l = l0, f = l0 / a.per, group_left = 0, seg_rows = 0;
-    for (int i = 0; i < iters; ++i) {
-        prefetch();
-        const bool row = WIDE || i < n;
-        if (row && group_left == 0) {
-            group_left = a.per - (l - f * a.per);
-            seg_rows = 0;
+    int b = at.b0, l = at.l0, f = at.l0 / a.per, group_left = 0, seg_rows = 0;
+    auto modulation = [&]() {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = c0 + v * step;
-                if (!on[v]) continue;
-                if (HASY) {
-                    const Vec w = load_any(a.post_weight, c, a.w_dtype, 1.f);
-                    const Vec g = load_any(a.gate.p, b * a.gate.b + f * a.gate.f + c, a.mod_dtype, 1.f);
+        for (int v = 0; v < V; ++v) {
+            const int c = c0 + v * step;
+            if (!on[v]) continue;
+            if (Y) {
+                const Vec w = load_any<SPLIT>(a.post_weight, c, a.w_dtype, 1.f, gap);
+                const Vec g = load_any<SPLIT>(a.gate.p, b * a.gate.b + f * a.gate.f + c, a.mod_dtype, 1.f, gap);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) cg[v].f[e] = mul2(w.f[e], g.f[e]);
-                }
-                const Vec w = load_any(a.weight, c, a.w_dtype, 1.f);
-                const Vec sc = load_any(a.scale.p, b * a.scale.b + f * a.scale.f + c, a.mod_dtype, 0.f);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) ca[v].f[e] = fma2(w.f[e], sc.f[e], w.f[e]);
+                for (int e = 0; e < 4; ++e) cg[v].f[e] = mul2(w.f[e], g.f[e]);
             }
+            const Vec w = load_any<SPLIT>(a.weight, c, a.w_dtype, 1.f, gap);
+            const Vec sc = load_any<SPLIT>(a.scale.p, b * a.scale.b + f * a.scale.f + c, a.mod_dtype, 0.f, gap);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ca[v].f[e] = fma2(w.f[e], sc.f[e], w.f[e]);
         }
-        if (row && group_left == 1 && i + 1 < n) {
-            const bool wrap = l + 1 == a.tokens;
-            const int nb = wrap ? b + 1 : b, nf = wrap ? 0 : f + 1;
+    };
+    // Rows [r0, r0 + R) of the step.  Of a row only o stays in registers across a sum; the rest is read again
+    // from the ring where it is needed, which costs less than the registers to keep it.
+    auto rows = [&](auto count, int r0, bool valid) {
+        constexpr int R = decltype(count)::value;
+        Vec o[R][V];  // rs x + gate wp yh, then t, the gradient that reaches it
+        [[maybe_unused]] float ry[R];
+        if constexpr (Y == 2) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = c0 + v * step;
-                if (!on[v]) continue;
-                if (HASY) prefetch_mod(a.gate, a.mod_dtype, nb, nf, c);
-                prefetch_mod(a.scale, a.mod_dtype, nb, nf, c);
-            }
-        }
-        ring_wait(a.stages);
-        Vec o[V];
-        float2 ry = both(1.f);
-        if (HASY && a.post) {
-            float2 acc = both(0.f);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const Vec y = ring.read<TB>(v * ONE + Y);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc = fma2(y.f[e], y.f[e], acc);
-            }
-            float q[1] = {fold(acc)};
-            team.sum(q);
-            ry = both(rsqrtf(q[0] * inv + a.post_eps));
-        }
-        // o: the sum rs x + gate wp yh, then t, the gradient that reaches it; the other rows are read again
-        // from the ring where they are needed, which costs less than the registers to keep them
-        float2 rr = both(0.f), mr = both(0.f), c0r = both(0.f), c1r = both(0.f);
-        if (has_dh) {
-            const float2 rs = both(a.rs);
-            float2 s1 = both(0.f), s2 = both(0.f), s3 = both(0.f), s4 = both(0.f);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                o[v] = ring.read<TS>(v * ONE);
-                if (HASY) {
-                    const Vec y = ring.read<TB>(v * ONE + Y);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[v].f[e] = fma2(cg[v].f[e], mul2(y.f[e], ry), mul2(rs, o[v].f[e]));
-                }
-                const Vec dh = ring.read<TB>(v * ONE + DH);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 d = mul2(dh.f[e], ca[v].f[e]);
-                    s1 = add2(s1, o[v].f[e]);
-                    s2 = fma2(o[v].f[e], o[v].f[e], s2);
-                    s3 = add2(s3, d);
-                    s4 = fma2(o[v].f[e], d, s4);
-                }
-            }
-            float q[4] = {fold(s1), fold(s2), fold(s3), fold(s4)}, m, r;
-            team.sum(q);
-            const bool centre = row_moments(q[0], q[1], inv, a.eps, layer, m, r);
-            const float am = layer ? q[2] * inv : 0.f;
-            float an = fmaf(-m, q[2], q[3]);  // sum of a (o - m)
-            if (WIDE ? centre : __any_sync(0xffffffffu, centre)) {
-                float c[2] = {0.f, 0.f};
+            for (int r = 0; r < R; ++r) {
+                float2 acc = both(0.f);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    if (!on[v]) continue;
-                    const Vec dh = ring.read<TB>(v * ONE + DH);
+                    const Vec y = ring.read<TB>(((r0 + r) * V + v) * ONE + YU);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc = fma2(y.f[e], y.f[e], acc);
+                }
+                ry[r] = fold(acc);
+            }
+            team.sum(ry);
+#pragma unroll
+            for (int r = 0; r < R; ++r) ry[r] = rsqrtf(ry[r] * inv + a.post_eps);
+        }
+        float rd[R], mr[R], k1[R], k0[R];
+        if (has_dh) {
+            float q[4 * R], m[R], am[R], an[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float2 s1 = both(0.f), s2 = both(0.f), s3 = both(0.f), s4 = both(0.f);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const int u = ((r0 + r) * V + v) * ONE;
+                    o[r][v] = ring.read<TS>(u);
+                    if constexpr (Y != 0) {
+                        Vec y = ring.read<TB>(u + YU);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (Y == 2) y.f[e] = mul2(y.f[e], both(ry[r]));
+                            if (scaled) o[r][v].f[e] = mul2(o[r][v].f[e], both(a.rs));
+                            o[r][v].f[e] = fma2(cg[v].f[e], y.f[e], o[r][v].f[e]);
+                        }
+                    }
+                    const Vec dh = ring.read<TB>(u + DH);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float2 d = add2(o[v].f[e], both(-m));
-                        c[0] += fold(mul2(d, d));
-                        c[1] += fold(mul2(d, mul2(dh.f[e], ca[v].f[e])));
+                        const float2 d = mul2(dh.f[e], ca[v].f[e]);
+                        s1 = add2(s1, o[r][v].f[e]);
+                        s2 = fma2(o[r][v].f[e], o[r][v].f[e], s2);
+                        s3 = add2(s3, d);
+                        s4 = fma2(o[r][v].f[e], d, s4);
+                    }
+                }
+                q[4 * r] = fold(s1), q[4 * r + 1] = fold(s2), q[4 * r + 2] = fold(s3), q[4 * r + 3] = fold(s4);
+            }
+            team.sum(q);
+            bool any = false, centre[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                centre[r] = row_moments(q[4 * r], q[4 * r + 1], inv, a.eps, layer, m[r], rd[r]);
+                any |= centre[r];
+                am[r] = layer ? q[4 * r + 2] * inv : 0.f;
+                an[r] = fmaf(-m[r], q[4 * r + 2], q[4 * r + 3]);  // sum of a (o - m)
+            }
+            if (WIDE ? any : __any_sync(0xffffffffu, any)) {
+                float c[2 * R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    c[2 * r] = c[2 * r + 1] = 0.f;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        if (!on[v]) continue;
+                        const Vec dh = ring.read<TB>(((r0 + r) * V + v) * ONE + DH);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 d = add2(o[r][v].f[e], both(-m[r]));
+                            c[2 * r] += fold(mul2(d, d));
+                            c[2 * r + 1] += fold(mul2(d, mul2(dh.f[e], ca[v].f[e])));
+                        }
                     }
                 }
                 team.sum(c);
-                if (centre) r = rsqrtf(c[0] * inv + a.eps), an = c[1];
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    if (centre[r]) rd[r] = rsqrtf(c[2 * r] * inv + a.eps), an[r] = c[2 * r + 1];
             }
-            an *= r * inv;  // mean(a n)
-            // r (a - am - n an) = r a + c1 o + c0 with n = o r - m r
-            rr = both(r), mr = both(-m * r);
-            c1r = both(-r * r * an), c0r = both(r * (m * r * an - am));
-        }
-        float2 su = both(0.f);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            Vec d = has_dxo ? ring.read<TS>(v * ONE + DXO) : vec_of(0.f);
-            if (has_dh) {
-                const Vec dh = ring.read<TB>(v * ONE + DH);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (row) {
-                        const float2 nrm = fma2(o[v].f[e], rr, mr);
-                        p0[v].f[e] = add2(p0[v].f[e], dh.f[e]);
-                        p1[v].f[e] = fma2(dh.f[e], nrm, p1[v].f[e]);
-                    }
-                    const float2 step_o = fma2(o[v].f[e], c1r, c0r);
-                    o[v].f[e] = add2(d.f[e], fma2(mul2(dh.f[e], ca[v].f[e]), rr, step_o));
-                }
-            } else {
-                o[v] = d;
-            }
-            const float2 rs = both(a.rs);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) d.f[e] = mul2(rs, o[v].f[e]);
-            if (row && on[v]) store_vec(pdx.p + v * step, d);
-            if (HASY) {
-                const Vec y = ring.read<TB>(v * ONE + Y);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 yh = mul2(y.f[e], ry);
-                    if (row) pq[v].f[e] = fma2(o[v].f[e], yh, pq[v].f[e]);
-                    o[v].f[e] = mul2(o[v].f[e], cg[v].f[e]);
-                    if (a.post) su = fma2(o[v].f[e], yh, su);
-                }
-                if (!a.post && row && on[v]) store_vec(pdy.p + v * step, o[v]);
+            for (int r = 0; r < R; ++r) {
+                // with n = o rd + mr: rd (a - am - n mean(a n)) = rd a + k1 o + k0
+                const float mean_an = an[r] * rd[r] * inv;
+                mr[r] = -m[r] * rd[r];
+                k1[r] = -rd[r] * rd[r] * mean_an;
+                k0[r] = -rd[r] * fmaf(mr[r], mean_an, am[r]);
             }
         }
-        if (HASY && a.post) {
-            float q[1] = {fold(su)};
-            team.sum(q);
-            const float2 mu = both(-q[0] * inv * ry.x);
+        float su[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float2 acc = both(0.f);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const Vec y = ring.read<TB>(v * ONE + Y);
+                const int u = ((r0 + r) * V + v) * ONE;
+                Vec d = has_dxo ? ring.read<TS>(u + DXO) : vec_of(0.f);
+                if (has_dh) {
+                    const Vec dh = ring.read<TB>(u + DH);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[v].f[e] = mul2(ry, fma2(y.f[e], mu, o[v].f[e]));
-                if (row && on[v]) store_vec(pdy.p + v * step, o[v]);
-            }
-        }
-        ring.done();
-        if (row) {
-            ++seg_rows;
-            if (group_left == 1 || i + 1 == n) {
-                // end of the modulation row, or of this worker's part of it: the sums go straight to the
-                // gradients where the worker had all its rows, else to the worker's first or last slot
-                const bool whole = seg_rows == a.per;
-                const long long slot = 2ll * worker + (i + 1 != seg_rows ? 1 : 0);
-                const long long g = (static_cast<long long>(b) * a.groups + f) * a.channels;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const int c = c0 + v * step;
-                    if (!on[v]) continue;
-                    if (!whole && a.part) {
-                        float* part = a.part + slot * 3 * a.channels + c;
-                        store_vec(part, p0[v]);
-                        store_vec(part + a.channels, p1[v]);
-                        store_vec(part + 2 * a.channels, pq[v]);
+                    for (int e = 0; e < 4; ++e) {
+                        if (valid) {
+                            p0[v].f[e] = add2(p0[v].f[e], dh.f[e]);
+                            p1[v].f[e] = fma2(dh.f[e], fma2(o[r][v].f[e], both(rd[r]), both(mr[r])), p1[v].f[e]);
+                        }
+                        d.f[e] = add2(d.f[e], fma2(o[r][v].f[e], both(k1[r]), both(k0[r])));
+                        o[r][v].f[e] = fma2(mul2(dh.f[e], ca[v].f[e]), both(rd[r]), d.f[e]);
                     }
-                    if (whole) {
-                        if (a.dshift) store_vec(a.dshift + g + c, p0[v]);
-                        if (a.dscale) {
-                            const Vec w = load_any(a.weight, c, a.w_dtype, 1.f), z = load_any(a.bias, c, a.w_dtype, 0.f);
-                            Vec d;
+                } else {
+                    o[r][v] = d;
+                }
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) d.f[e] = fma2(w.f[e], p1[v].f[e], mul2(z.f[e], p0[v].f[e]));
-                            store_vec(a.dscale + g + c, d);
-                        }
-                        if (HASY && a.dgate) {
-                            Vec d = load_any(a.post_weight, c, a.w_dtype, 1.f);
+                for (int e = 0; e < 4; ++e) d.f[e] = scaled ? mul2(both(a.rs), o[r][v].f[e]) : o[r][v].f[e];
+                if (valid && on[v]) store_vec<TS, SPLIT>(pdx.at(r, c0 + v * step), d, gap);
+                if constexpr (Y != 0) {
+                    Vec y = ring.read<TB>(u + YU);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) d.f[e] = mul2(d.f[e], pq[v].f[e]);
-                            store_vec(a.dgate + g + c, d);
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        if (Y == 2) y.f[e] = mul2(y.f[e], both(ry[r]));
+                        if (valid) pq[v].f[e] = fma2(o[r][v].f[e], y.f[e], pq[v].f[e]);
+                        o[r][v].f[e] = mul2(o[r][v].f[e], cg[v].f[e]);
+                        if (Y == 2) acc = fma2(o[r][v].f[e], y.f[e], acc);
                     }
-                    if (a.wpart) {
-                        float* ws = wsum + v * wv;
-                        const Vec sc = load_any(a.scale.p, b * a.scale.b + f * a.scale.f + c, a.mod_dtype, 0.f);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 d1 = fma2(sc.f[e], p1[v].f[e], p1[v].f[e]), d0 = fma2(sc.f[e], p0[v].f[e], p0[v].f[e]);
-                            ws[2 * e * we] += d1.x, ws[(2 * e + 1) * we] += d1.y;
-                            ws[wk + 2 * e * we] += d0.x, ws[wk + (2 * e + 1) * we] += d0.y;
-                        }
-                        if (HASY) {
-                            const Vec gt = load_any(a.gate.p, b * a.gate.b + f * a.gate.f + c, a.mod_dtype, 1.f);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float2 d = mul2(gt.f[e], pq[v].f[e]);
-                                ws[2 * wk + 2 * e * we] += d.x, ws[2 * wk + (2 * e + 1) * we] += d.y;
-                            }
-                        }
-                    }
-                    p0[v] = p1[v] = pq[v] = vec_of(0.f);
+                    if (Y == 1 && valid && on[v]) store_vec<TB, SPLIT>(pdy.at(r, c0 + v * step), o[r][v], gap);
                 }
             }
-            --group_left;
-            ++l;
-            pdx.next(a.dx);
-            if (HASY) pdy.next(a.dy);
-            if (group_left == 0) ++f;
+            su[r] = fold(acc);
+        }
+        if constexpr (Y == 2) {
+            team.sum(su);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    const Vec y = ring.read<TB>(((r0 + r) * V + v) * ONE + YU);
+                    const float2 mu = both(-su[r] * inv * ry[r]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[r][v].f[e] = mul2(both(ry[r]), fma2(y.f[e], mu, o[r][v].f[e]));
+                    if (valid && on[v]) store_vec<TB, SPLIT>(pdy.at(r, c0 + v * step), o[r][v], gap);
+                }
+        }
+    };
+    // The end of the modulation row, or of this worker's part of it (`ended` of its rows done): the sums go
+    // straight to the gradients where the worker had all its rows, else to the worker's first or last slot.
+    auto flush = [&](int ended) {
+        const bool whole = seg_rows == a.per;
+        const long long slot = 2ll * at.worker + (ended != seg_rows ? 1 : 0);
+        const long long g = (static_cast<long long>(b) * a.groups + f) * a.channels;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = c0 + v * step;
+            if (!on[v]) continue;
+            if (!whole && a.part) {
+                float* part = a.part + slot * 3 * a.channels + c;
+                store_vec<float, SPLIT>(part, p0[v], gap);
+                store_vec<float, SPLIT>(part + a.channels, p1[v], gap);
+                store_vec<float, SPLIT>(part + 2 * a.channels, pq[v], gap);
+            }
+            if (whole) {
+                if (a.dshift) store_vec<float, SPLIT>(a.dshift + g + c, p0[v], gap);
+                if (a.dscale) {
+                    const Vec w = load_any<SPLIT>(a.weight, c, a.w_dtype, 1.f, gap);
+                    const Vec z = load_any<SPLIT>(a.bias, c, a.w_dtype, 0.f, gap);
+                    Vec d;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d.f[e] = fma2(w.f[e], p1[v].f[e], mul2(z.f[e], p0[v].f[e]));
+                    store_vec<float, SPLIT>(a.dscale + g + c, d, gap);
+                }
+                if (Y && a.dgate) {
+                    Vec d = load_any<SPLIT>(a.post_weight, c, a.w_dtype, 1.f, gap);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) d.f[e] = mul2(d.f[e], pq[v].f[e]);
+                    store_vec<float, SPLIT>(a.dgate + g + c, d, gap);
+                }
+            }
+            if (a.wpart) {
+                const Vec sc = load_any<SPLIT>(a.scale.p, b * a.scale.b + f * a.scale.f + c, a.mod_dtype, 0.f, gap);
+                const Vec gt = load_any<SPLIT>(a.gate.p, b * a.gate.b + f * a.gate.f + c, a.mod_dtype, 1.f, gap);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    add_weights(0, v, e, fma2(sc.f[e], p1[v].f[e], p1[v].f[e]));
+                    add_weights(1, v, e, fma2(sc.f[e], p0[v].f[e], p0[v].f[e]));
+                    if (Y) add_weights(2, v, e, mul2(gt.f[e], pq[v].f[e]));
+                }
+            }
+            p0[v] = p1[v] = pq[v] = vec_of(0.f);
+        }
+        seg_rows = 0;
+    };
+    auto advance = [&](int R, int ended) {
+        seg_rows += R;
+        group_left -= R;
+        if (group_left == 0 || ended == at.n) flush(ended);
+        l += R;
+        pdx.next(R);
+        if (Y) pdy.next(R);
+        if (group_left == 0) {
+            ++f;
             if (l == a.tokens) {
                 l = f = 0;
                 ++b;
-                pdx.wrap(a.dx, a.tokens);
-                if (HASY) pdy.wrap(a.dy, a.tokens);
+                pdx.wrap();
+                if (Y) pdy.wrap();
             }
         }
+    };
+
+    for (int i = 0; i < at.longest; i += ROWS) {
+        prefetch();
+        ring_wait(a.stages);
+        const int rest = at.n - i;
+        if (WIDE && ROWS > 1 && rest >= ROWS && group_left >= ROWS) {
+            rows(Count<ROWS>{}, 0, true);
+            advance(ROWS, i + ROWS);
+        } else {
+#pragma unroll 1
+            for (int r = 0; r < ROWS; ++r) {
+                const bool valid = r < rest;
+                if (WIDE && !valid) break;
+                if (valid && group_left == 0) {
+                    modulation();
+                    group_left = a.per - (l - f * a.per);
+                }
+                if (valid && group_left == 1 && rest > r + 1) {
+                    const bool wrap = l + 1 == a.tokens;
+                    const int nb = wrap ? b + 1 : b, nf = wrap ? 0 : f + 1;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const int c = c0 + v * step;
+                        if (!on[v]) continue;
+                        if (Y) prefetch_mod<SPLIT>(a.gate, a.mod_dtype, nb, nf, c, gap);
+                        prefetch_mod<SPLIT>(a.scale, a.mod_dtype, nb, nf, c, gap);
+                    }
+                }
+                rows(Count<1>{}, r, valid);
+                if (valid) advance(1, i + r + 1);
+            }
+        }
+        ring.done();
     }
     if (a.wpart && a.wsum_shared)
-        for (int v = 0; v < V && c0 + v * step < a.channels; ++v)
+        for (int v = 0; v < V && on[v]; ++v)
             for (int k = 0; k < 3; ++k)
-                for (int e = 0; e < 8; ++e) wslot[k * a.channels + v * step + e] = wsum[k * wk + v * wv + e * we];
+                for (int e = 0; e < 8; ++e)
+                    wslot[k * a.channels + v * step + e + (e < 4 ? 0 : gap - 4)] = wsum[k * wk + v * wv + e * we];
 }
 
 // The sums over tokens that more than one worker took part in: 32 channels a block, the partial sums
-// split over its 16 warps and joined in a fixed order.  Blocks y < groups join a modulation row's slots
-// (y counts modulation rows, or the workers' boundaries where those are fewer), the last one the
-// weights' sums.
+// split over its warps and joined in a fixed order.  Blocks y < jobs join a modulation row's slots (y counts
+// modulation rows, or the workers' boundaries where those are fewer), the one after them the weights' sums.
 constexpr int kFinalWarps = 16;
 
 __global__ void __launch_bounds__(32 * kFinalWarps) residual_norm_final_kernel(const __grid_constant__ ResidualNormArgs a,
                                                                                int jobs, int by_boundary) {
     __shared__ float red[3][kFinalWarps][32];
+    __shared__ int w_first, w_last, w_second;
+    __shared__ long long group;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     const bool in = c < a.channels;
     const bool weights = static_cast<int>(blockIdx.y) == jobs;
-    int w0 = 0, w1 = a.workers - 1;
-    long long g = 0;
-    if (!weights) {
-        g = blockIdx.y;
-        if (by_boundary) {  // the modulation row that worker y + 1's first row continues
-            const long long r = worker_lo(a.rows, a.workers, static_cast<int>(blockIdx.y) + 1);
-            g = r / a.per;
-            if (g * a.per == r || r == a.rows) return;
-        }
-        w0 = worker_of(a.rows, a.workers, g * a.per);
-        w1 = worker_of(a.rows, a.workers, (g + 1) * a.per - 1);
-        if (w0 == w1) return;
-    }
-    float sum[3] = {0.f, 0.f, 0.f};
-    if (in)
-        for (int w = w0 + warp; w <= w1; w += kFinalWarps) {
-            const float* p;
-            if (weights) {
-                p = a.wpart + static_cast<long long>(w) * 3 * a.channels + c;
-            } else {
-                if (worker_lo(a.rows, a.workers, w) == worker_lo(a.rows, a.workers, w + 1)) continue;
-                const int last = worker_lo(a.rows, a.workers, w) < g * a.per ? 1 : 0;
-                p = a.part + (2ll * w + last) * 3 * a.channels + c;
+    if (threadIdx.x == 0) {
+        w_first = 0, w_last = a.workers - 1, w_second = -1, group = 0;
+        if (!weights) {
+            long long g = blockIdx.y;
+            bool whole = false;
+            if (by_boundary) {  // the modulation row that worker y + 1's first row continues
+                const long long r = worker_lo(a.rows, a.workers, static_cast<int>(blockIdx.y) + 1);
+                g = r / a.per;
+                whole = g * a.per == r || r == a.rows;
             }
+            if (!whole) {
+                w_first = worker_of(a.rows, a.workers, g * a.per);
+                w_last = worker_of(a.rows, a.workers, (g + 1) * a.per - 1);
+                // its sums are in the workers' first slots, but in the second one of a worker that came to
+                // it from another row
+                if (worker_lo(a.rows, a.workers, w_first) < g * a.per) w_second = w_first;
+                group = g;
+            }
+            if (whole || w_first == w_last) w_last = -1;  // one worker had it all
+        }
+    }
+    __syncthreads();
+    const int w0 = w_first, w1 = w_last, second = w_second;
+    const long long g = group;
+    if (w1 < 0) return;
+    float sum[3] = {0.f, 0.f, 0.f};
+    if (in) {
+        const bool all = weights || a.workers <= a.rows;  // else some workers had no rows and wrote nothing
+        const long long row = 3ll * a.channels;
+#pragma unroll 4
+        for (int w = w0 + warp; w <= w1; w += kFinalWarps) {
+            if (!all && worker_lo(a.rows, a.workers, w) == worker_lo(a.rows, a.workers, w + 1)) continue;
+            const float* p = weights ? a.wpart + w * row + c : a.part + (2ll * w + (w == second ? 1 : 0)) * row + c;
 #pragma unroll
             for (int k = 0; k < 3; ++k) sum[k] += p[static_cast<long long>(k) * a.channels];
         }
+    }
 #pragma unroll
     for (int k = 0; k < 3; ++k) red[k][warp][lane] = sum[k];
     __syncthreads();
@@ -624,29 +744,36 @@ cudaError_t launch(K kernel, const ResidualNormArgs& a, const RowPlan& p, size_t
     return cudaGetLastError();
 }
 
-template <typename TS, typename TB, int V, bool WIDE>
+// The backward takes two rows a step where the ring holds two such steps.
+template <typename TS, typename TB, int V, int Y, bool WIDE>
 cudaError_t launch_dir(ResidualNormArgs a, const RowPlan& p, bool backward, cudaStream_t st) {
-    const bool y = a.y.p != nullptr;
-    const int units = backward ? 2 * kUnits<TS> + (y ? 2 : 1) * kUnits<TB> : kUnits<TS> + (y ? kUnits<TB> : 0);
-    const size_t stage = size_t(16) * V * units * p.threads, sums = size_t(3) * V * 32 * p.threads;
+    const int units = backward ? 2 * kUnits<TS> + (Y ? 2 : 1) * kUnits<TB> : kUnits<TS> + (Y ? kUnits<TB> : 0);
+    const size_t row = size_t(16) * V * units * p.threads, sums = size_t(3) * V * 32 * p.threads;
     const int per_sm = blocks_per_sm(p, backward);
     const size_t room = kRingBytes / per_sm;
-    a.stages = ring_stages(stage, per_sm, room);
+    const int rows = WIDE && backward && 4 * row <= room ? 2 : 1;
+    a.stages = ring_stages(rows * row, per_sm, room, (a.rows + a.workers - 1) / a.workers, rows);
     // the weights' sums take what the ring leaves
-    a.wsum_shared = backward && a.wpart && a.stages * stage + sums <= room;
-    const size_t smem = a.stages * stage + (a.wsum_shared ? sums : 0);
-    if (!backward)
-        return y ? launch(residual_norm_fwd_kernel<TS, TB, V, true, WIDE>, a, p, smem, st)
-                 : launch(residual_norm_fwd_kernel<TS, TB, V, false, WIDE>, a, p, smem, st);
-    return y ? launch(residual_norm_bwd_kernel<TS, TB, V, true, WIDE>, a, p, smem, st)
-             : launch(residual_norm_bwd_kernel<TS, TB, V, false, WIDE>, a, p, smem, st);
+    a.wsum_shared = backward && a.wpart && a.stages * rows * row + sums <= room;
+    const size_t smem = a.stages * rows * row + (a.wsum_shared ? sums : 0);
+    if (!backward) return launch(residual_norm_fwd_kernel<TS, TB, V, Y, WIDE, 1>, a, p, smem, st);
+    if constexpr (WIDE) {
+        if (rows == 2) return launch(residual_norm_bwd_kernel<TS, TB, V, Y, WIDE, 2>, a, p, smem, st);
+    }
+    return launch(residual_norm_bwd_kernel<TS, TB, V, Y, WIDE, 1>, a, p, smem, st);
+}
+template <typename TS, typename TB, int V, bool WIDE>
+cudaError_t launch_y(const ResidualNormArgs& a, const RowPlan& p, bool backward, cudaStream_t st) {
+    return a.y.p == nullptr      ? launch_dir<TS, TB, V, 0, WIDE>(a, p, backward, st)
+           : a.post == kNormNone ? launch_dir<TS, TB, V, 1, WIDE>(a, p, backward, st)
+                                 : launch_dir<TS, TB, V, 2, WIDE>(a, p, backward, st);
 }
 
 template <typename TS, typename TB>
 cudaError_t launch_types(const ResidualNormArgs& a, const RowPlan& p, bool backward, cudaStream_t st) {
-    return p.team <= 32 ? launch_dir<TS, TB, 1, false>(a, p, backward, st)
-           : p.V == 1   ? launch_dir<TS, TB, 1, true>(a, p, backward, st)
-                        : launch_dir<TS, TB, 2, true>(a, p, backward, st);
+    return p.team <= 32 ? launch_y<TS, TB, 1, false>(a, p, backward, st)
+           : p.V == 1   ? launch_y<TS, TB, 1, true>(a, p, backward, st)
+                        : launch_y<TS, TB, 2, true>(a, p, backward, st);
 }
 
 }  // namespace

@@ -116,28 +116,43 @@ __device__ __forceinline__ void pack<float>(const Vec& v, uint4 (&u)[2]) {
                           __float_as_uint(v.f[2 * i + 1].x), __float_as_uint(v.f[2 * i + 1].y));
 }
 
-template <typename T>
-__device__ __forceinline__ Vec load_vec(const T* p) {
+// A vector's eight elements in memory are consecutive, or (SPLIT) two runs of four, the second `gap`
+// elements on.  Split vectors serve rotary pairs of a head's two halves, and rows in fp32: there a warp's
+// 16-byte accesses then cover consecutive memory, where eight consecutive elements a thread would touch
+// every line twice.
+template <typename T, bool SPLIT = false>
+__device__ __forceinline__ Vec load_vec(const T* p, int gap = 4) {
     uint4 u[kUnits<T>];
+    if constexpr (SPLIT && sizeof(T) == 2) {
+        const uint2 a = __ldg(reinterpret_cast<const uint2*>(p)), b = __ldg(reinterpret_cast<const uint2*>(p + gap));
+        u[0] = make_uint4(a.x, a.y, b.x, b.y);
+    } else {
 #pragma unroll
-    for (int i = 0; i < kUnits<T>; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        for (int i = 0; i < kUnits<T>; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(p + i * (SPLIT ? gap : 4)));
+    }
     return unpack<T>(u);
 }
-template <typename T>
-__device__ __forceinline__ void store_vec(T* p, const Vec& v) {
+template <typename T, bool SPLIT = false>
+__device__ __forceinline__ void store_vec(T* p, const Vec& v, int gap = 4) {
     uint4 u[kUnits<T>];
     pack<T>(v, u);
+    if constexpr (SPLIT && sizeof(T) == 2) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(u[0].x, u[0].y);
+        *reinterpret_cast<uint2*>(p + gap) = make_uint2(u[0].z, u[0].w);
+    } else {
 #pragma unroll
-    for (int i = 0; i < kUnits<T>; ++i) reinterpret_cast<uint4*>(p)[i] = u[i];
+        for (int i = 0; i < kUnits<T>; ++i) *reinterpret_cast<uint4*>(p + i * (SPLIT ? gap : 4)) = u[i];
+    }
 }
 
 // Eight elements of a vector whose type is known at run time (weights, modulation rows), or `fill`
 // where there is no such vector.
-__device__ __forceinline__ Vec load_any(const void* base, long long at, int dtype, float fill) {
+template <bool SPLIT = false>
+__device__ __forceinline__ Vec load_any(const void* base, long long at, int dtype, float fill, int gap = 4) {
     if (!base) return vec_of(fill);
-    if (dtype == kF32) return load_vec(static_cast<const float*>(base) + at);
-    if (dtype == kBf16) return load_vec(static_cast<const __nv_bfloat16*>(base) + at);
-    return load_vec(static_cast<const __half*>(base) + at);
+    if (dtype == kF32) return load_vec<float, SPLIT>(static_cast<const float*>(base) + at, gap);
+    if (dtype == kBf16) return load_vec<__nv_bfloat16, SPLIT>(static_cast<const __nv_bfloat16*>(base) + at, gap);
+    return load_vec<__half, SPLIT>(static_cast<const __half*>(base) + at, gap);
 }
 
 // Asynchronous copies global -> shared.  Every thread reads back only what it copied itself, so its own
@@ -176,10 +191,15 @@ struct Ring {
     }
     __device__ __forceinline__ void filled() { in = in == last ? first : in + stage; }
     __device__ __forceinline__ void done() { out = out == last ? first : out + stage; }
-    template <typename T>
-    __device__ __forceinline__ void copy(int u, const T* p) const {
+    template <bool SPLIT = false, typename T>
+    __device__ __forceinline__ void copy(int u, const T* p, int gap = 4) const {
+        if constexpr (SPLIT && sizeof(T) == 2) {
+            async_copy8(in + u * unit, p);
+            async_copy8(in + u * unit + 8, p + gap);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kUnits<T>; ++i) async_copy16(in + (u + i) * unit, reinterpret_cast<const uint4*>(p) + i);
+            for (int i = 0; i < kUnits<T>; ++i) async_copy16(in + (u + i) * unit, p + i * (SPLIT ? gap : 4));
+        }
     }
     template <typename T>
     __device__ __forceinline__ Vec read(int u) const {
@@ -198,22 +218,24 @@ struct Ring {
     }
 };
 
-// A row's copy is committed `stages` - 1 rows ahead; the oldest has arrived.
+// A step's copies are committed `stages` - 1 steps ahead (1 to 4 stages); the oldest have arrived.
 __device__ __forceinline__ void ring_wait(int stages) {
-    switch (stages) {
-        case 1: async_wait<0>(); break;
-        case 2: async_wait<1>(); break;
-        case 3: async_wait<2>(); break;
-        case 4: async_wait<3>(); break;
-        case 5: async_wait<4>(); break;
-        default: async_wait<5>(); break;
-    }
+    if (stages == 3) async_wait<2>();
+    else if (stages == 4) async_wait<3>();
+    else if (stages == 2) async_wait<1>();
+    else async_wait<0>();
 }
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 4;
+
+// A compile-time count as an argument.
+template <int N>
+struct Count {
+    static constexpr int value = N;
+};
 
 // A team of threads shares a row: the whole block (WIDE; a multiple of 32 threads, at most 1024), or
 // `size` threads of a warp, a power of two (then several teams in a block).
-constexpr int kTeamScratch = 2 * 4 * 32;  // floats of shared memory for a block-wide team's sums
+constexpr int kTeamScratch = 2 * 8 * 32;  // floats of shared memory for a block-wide team's sums
 
 template <bool WIDE>
 struct Team {
@@ -234,13 +256,13 @@ struct Team {
     static __device__ __forceinline__ float swap(float x, int o) { return __shfl_xor_sync(0xffffffffu, x, o); }
 
     // Every value summed over the team, in a fixed order; each thread gets the sums.  In a warp, lanes that
-    // exchange two or four values keep half of them each time, so that four values cost six shuffles and
-    // end in eight lanes each.  Across warps: one write, one barrier, and each lane adds four warps' values.
-    // Consecutive sums use the scratch's halves in turn: before a thread can write a half again, every
-    // thread has passed the other half's barrier and so has read this one.
+    // exchange several values keep half of them each time, so that eight values cost nine shuffles and end
+    // in four lanes each.  Across warps: one write, one barrier, and each lane adds its share of the warps'
+    // values.  Consecutive sums use the scratch's halves in turn: before a thread can write a half again,
+    // every thread has passed the other half's barrier and so has read this one.
     template <int N>
     __device__ __forceinline__ void sum(float (&v)[N]) {
-        static_assert(N == 1 || N == 2 || N == 4, "");
+        static_assert(N == 1 || N == 2 || N == 4 || N == 8, "");
         if (!WIDE) {
             for (int o = size >> 1; o > 0; o >>= 1)
 #pragma unroll
@@ -248,36 +270,64 @@ struct Team {
             return;
         }
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        float k;
-        if constexpr (N == 4) {
-            const bool up = lane & 16, right = lane & 8;
-            const float a = (up ? v[2] : v[0]) + swap(up ? v[0] : v[2], 16);
-            const float b = (up ? v[3] : v[1]) + swap(up ? v[1] : v[3], 16);
-            k = (right ? b : a) + swap(right ? a : b, 8);
-        } else if constexpr (N == 2) {
-            const bool up = lane & 16;
-            k = (up ? v[1] : v[0]) + swap(up ? v[0] : v[1], 16);
-            k += swap(k, 8);
-        } else {
-            k = v[0] + swap(v[0], 16);
-            k += swap(k, 8);
-        }
-        k += swap(k, 4);
-        k += swap(k, 2);
-        k += swap(k, 1);
-        constexpr int span = 32 / N;  // lanes a value
-        float* s = scratch + turn * (4 * 32);
-        turn ^= 1;
-        if (lane % span == 0) s[lane / span * 32 + warp] = k;
-        __syncthreads();
-        const float4 u = reinterpret_cast<const float4*>(s)[lane / span * 8 + (lane & 7)];
-        k = (u.x + u.y) + (u.z + u.w);
-        k += swap(k, 4);
-        k += swap(k, 2);
-        k += swap(k, 1);
+        float k[N];
 #pragma unroll
-        for (int n = 0; n < N; ++n) v[n] = N == 1 ? k : __shfl_sync(0xffffffffu, k, n * span);
+        for (int n = 0; n < N; ++n) k[n] = v[n];
+#pragma unroll
+        for (int o = 16, left = N; o > 0; o >>= 1) {
+            if (left > 1) {  // keep the upper or the lower half of the values
+                left >>= 1;
+                const bool up = lane & o;
+#pragma unroll
+                for (int n = 0; n < left; ++n) {
+                    const float give = up ? k[n] : k[n + left];
+                    k[n] = (up ? k[n + left] : k[n]) + swap(give, o);
+                }
+            } else {
+                k[0] += swap(k[0], o);
+            }
+        }
+        constexpr int span = 32 / N;  // lanes a value
+        float* s = scratch + turn * (8 * 32);
+        turn ^= 1;
+        if (lane % span == 0) s[lane / span * 32 + warp] = k[0];
+        __syncthreads();
+        // eight float4 of warps' values a sum: one a lane, or two where a sum has four lanes
+        const float4* f = reinterpret_cast<const float4*>(s) + lane / span * 8;
+        const float4 a = f[lane & (N == 8 ? 3 : 7)];
+        k[0] = (a.x + a.y) + (a.z + a.w);
+        if (N == 8) {
+            const float4 b = f[(lane & 3) + 4];
+            k[0] += (b.x + b.y) + (b.z + b.w);
+        } else {
+            k[0] += swap(k[0], 4);
+        }
+        k[0] += swap(k[0], 2);
+        k[0] += swap(k[0], 1);
+        const float all = k[0];
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] = N == 1 ? all : __shfl_sync(0xffffffffu, all, n * span);
     }
+};
+
+// Where a worker stands in a tensor of rows with free batch and token strides.  The same for all threads of
+// a block-wide team, so that it takes none of their registers.
+template <typename T>
+struct RowWalk {
+    char* p;
+    long long step, back;  // bytes to the next token, and from behind a sample's last token to the next sample
+    // element strides of batch and token; from token l of sample b
+    __device__ RowWalk(const void* base, long long sb, long long sl, int b, int l, int tokens)
+        : p(const_cast<char*>(static_cast<const char*>(base)) + (b * sb + l * sl) * static_cast<int>(sizeof(T))),
+          step(sl * static_cast<int>(sizeof(T))),
+          back((sb - tokens * sl) * static_cast<int>(sizeof(T))) {}
+    __device__ RowWalk(const RowTensor& t, int b, int l, int tokens) : RowWalk(t.p, t.b, t.l, b, l, tokens) {}
+    // element c of the row `r` rows on
+    __device__ __forceinline__ T* at(int r, int c) const {
+        return reinterpret_cast<T*>(p + r * step + static_cast<unsigned>(c * static_cast<int>(sizeof(T))));
+    }
+    __device__ __forceinline__ void next(int rows = 1) { p += rows * step; }
+    __device__ __forceinline__ void wrap() { p += back; }
 };
 
 // Rows [lo, hi) of worker w among `workers` workers sharing n rows; the worker that has row r.
@@ -304,13 +354,15 @@ inline void row_workers(long long rows, int most, RowPlan* p) {
     const long long want = (rows + teams - 1) / teams, cap = kMaxWorkers / teams < most ? kMaxWorkers / teams : most;
     p->blocks = static_cast<int>(want < cap ? want : cap);
     p->workers = p->blocks * teams;
+    p->parts = 1;
 }
-// Stages of a ring: enough that a processor's blocks keep 96 KB of copies in flight (about twice what its
-// share of the bandwidth moves in the time a load takes), within `room` bytes a block.
-inline int ring_stages(size_t stage, int blocks_per_sm, size_t room) {
+// Stages of a ring: enough that an SM's blocks keep 96 KB of copies in flight (about twice what its share of
+// the bandwidth moves in the time a load takes), within `room` bytes a block, and no more than a worker of
+// `most` rows takes steps of `rows`.
+inline int ring_stages(size_t stage, int blocks_per_sm, size_t room, long long most, int rows) {
     int n = 2;
     while (n < kMaxStages && (n - 1) * stage * blocks_per_sm < 96 * 1024) ++n;
-    while (n > 1 && n * stage > room) --n;
+    while (n > 1 && (n * stage > room || (n - 1ll) * rows >= most)) --n;
     return n;
 }
 

@@ -632,6 +632,14 @@ def _rows(c, name, t, shape, dtype, device, field):
     return t.data_ptr()
 
 
+def _like(t, shape, dtype):
+    """A new contiguous tensor of this shape on t's device (the quicker of torch's ways where t is one)."""
+    torch = _torch()
+    if t.is_contiguous():
+        return torch.empty_like(t) if t.dtype is dtype else torch.empty_like(t, dtype=dtype)
+    return torch.empty(shape, dtype=dtype, device=t.device)
+
+
 def _vector(name, t, n, dtype, device):
     if t.shape != (n,) or (dtype is not None and t.dtype is not dtype) or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {'' if dtype is None else str(dtype) + ' '}tensor of {n} elements "
@@ -731,7 +739,6 @@ def residual_norm_fwd(prob: ResidualNorm, x, y=None, gate=None, scale=None, shif
     (expanded views broadcast); weight, bias, post_weight: [channels].  h gets y's type, or h_dtype (a
     torch dtype; for a call without y, default x's).  Rows may be strided, x_out may be x and h may be y.
     Returns (x_out, h): x itself where there is no y, None for h with NORM_NONE."""
-    empty = _torch().empty
     row, device = prob[:3], x.device
     with _On(device, stream) as handle:
         c, block, px, py = _residual_norm_problem(prob, x, y, h, gate, scale, shift, weight, bias, post_weight)
@@ -743,7 +750,7 @@ def residual_norm_fwd(prob: ResidualNorm, x, y=None, gate=None, scale=None, shif
             if x_out is not None:
                 raise ValueError("x_out: there is no y to add")
         elif x_out is None:
-            x_out = empty(row, dtype=x.dtype, device=device)
+            x_out = _like(x, row, x.dtype)
             po = x_out.data_ptr()
         else:
             po = _rows(c, "x_out", x_out, row, x.dtype, device, "x_out_strides")
@@ -751,7 +758,7 @@ def residual_norm_fwd(prob: ResidualNorm, x, y=None, gate=None, scale=None, shif
             if h is not None:
                 raise ValueError("h: the problem has no norm")
         elif h is None:
-            h = empty(row, dtype=block, device=device)
+            h = _like(x if y is None else y, row, block)
             ph = h.data_ptr()
         else:
             ph = _rows(c, "h", h, row, block, device, "h_strides")
@@ -775,11 +782,11 @@ def residual_norm_bwd(prob: ResidualNorm, x, y=None, dh=None, dx_out=None, gate=
         pdh = None if dh is None else _rows(c, "dh", dh, row, block, device, "h_strides")
         pdo = None if dx_out is None else _rows(c, "dx_out", dx_out, row, x.dtype, device, "x_out_strides")
         if dx is None:
-            dx = empty(row, dtype=x.dtype, device=device)
+            dx = _like(x, row, x.dtype)
         pdx, pdy = _rows(c, "dx", dx, row, x.dtype, device, "dx_strides"), None
         if y is not None:
             if dy is None:
-                dy = empty(row, dtype=block, device=device)
+                dy = _like(y, row, block)
             pdy = _rows(c, "dy", dy, row, block, device, "dy_strides")
         elif dy is not None:
             raise ValueError("dy: there is no y")
@@ -874,7 +881,6 @@ def qk_rope_fwd(prob: QkRope, q, k=None, wq=None, wk=None, positions=None, out_q
     contiguous last dimension, e.g. views of a fused QKV tensor); wq, wk: the norm's weights ([head_dim], or
     [heads * head_dim] with QK_NORM_TOKEN); positions: int32 [1 or batch, tokens, 3] in place of the grid.
     out_q may be q and out_k may be k.  Returns (out_q, out_k); out_k is None without k."""
-    empty = _torch().empty
     device = q.device
     with _On(device, stream) as handle:
         c, pq, pk = _qk_rope_problem(prob, q, k, wq, wk, positions)
@@ -883,12 +889,12 @@ def qk_rope_fwd(prob: QkRope, q, k=None, wq=None, wk=None, positions=None, out_q
         c.out_dtype = c.x_dtype if code is None else code
         shape, po_k = (prob.batch, prob.tokens, prob.heads, prob.head_dim), None
         if out_q is None:
-            out_q = empty(shape, dtype=dtype, device=device)
+            out_q = _like(q, shape, dtype)
         po_q = _rows(c, "out_q", out_q, shape, dtype, device, "out_q_strides")
         if k is not None:
             shape = (prob.batch, prob.tokens, prob.kv_heads, prob.head_dim)
             if out_k is None:
-                out_k = empty(shape, dtype=dtype, device=device)
+                out_k = _like(k, shape, dtype)
             po_k = _rows(c, "out_k", out_k, shape, dtype, device, "out_k_strides")
         elif out_k is not None:
             raise ValueError("out_k: there is no k")
@@ -914,13 +920,13 @@ def qk_rope_bwd(prob: QkRope, q, k, dout_q, dout_k=None, wq=None, wk=None, posit
         shape, dwq, dwk, pgk, pdk = (prob.batch, prob.tokens, prob.heads, prob.head_dim), None, None, None, None
         pgq = _rows(c, "dout_q", dout_q, shape, None, device, "out_q_strides")
         if dq is None:
-            dq = empty(shape, dtype=q.dtype, device=device)
+            dq = _like(q, shape, q.dtype)
         pdq = _rows(c, "dq", dq, shape, q.dtype, device, "dq_strides")
         if k is not None:
             shape = (prob.batch, prob.tokens, prob.kv_heads, prob.head_dim)
             pgk = _rows(c, "dout_k", dout_k, shape, dout_q.dtype, device, "out_k_strides")
             if dk is None:
-                dk = empty(shape, dtype=q.dtype, device=device)
+                dk = _like(k, shape, k.dtype)
             pdk = _rows(c, "dk", dk, shape, q.dtype, device, "dk_strides")
         elif dk is not None:
             raise ValueError("dk: there is no k")

@@ -138,7 +138,8 @@ HEAD, TOKEN = slra.QK_NORM_HEAD, slra.QK_NORM_TOKEN
 @pytest.mark.parametrize("kw,status", [
     (dict(), slra.ERR_NO_DEVICE), (dict(batch=0), slra.ERR_INVALID_ARG), (dict(heads=0), slra.ERR_INVALID_ARG),
     (dict(kv_heads=-1), slra.ERR_INVALID_ARG), (dict(head_dim=60), slra.ERR_UNSUPPORTED),
-    (dict(head_dim=264), slra.ERR_UNSUPPORTED), (dict(heads=255, kv_heads=2), slra.ERR_UNSUPPORTED),
+    (dict(head_dim=264), slra.ERR_UNSUPPORTED), (dict(heads=129), slra.ERR_UNSUPPORTED), (dict(kv_heads=129), slra.ERR_UNSUPPORTED),
+    (dict(heads=128, kv_heads=128), slra.ERR_NO_DEVICE),
     (dict(heads=1 << 40), slra.ERR_UNSUPPORTED),
     (dict(batch=1 << 16, tokens=1 << 16), slra.ERR_INVALID_ARG), (dict(T=0), slra.ERR_INVALID_ARG),
     (dict(W=23), slra.ERR_INVALID_ARG), (dict(first_token=1), slra.ERR_INVALID_ARG),
@@ -147,7 +148,9 @@ HEAD, TOKEN = slra.QK_NORM_HEAD, slra.QK_NORM_TOKEN
     (dict(positions=at(8), positions_stride=71), slra.ERR_INVALID_ARG),
     (dict(positions=at(8), positions_stride=72), slra.ERR_NO_DEVICE), (dict(W=0, rotate=0), slra.ERR_NO_DEVICE),
     (dict(pos_offset=(0, (1 << 31) + 1, 0)), slra.ERR_INVALID_ARG), (dict(theta=float("nan")), slra.ERR_INVALID_ARG),
-    (dict(theta=-1.0), slra.ERR_INVALID_ARG), (dict(rope_split=(20, 10, 3)), slra.ERR_INVALID_ARG),
+    (dict(theta=-1.0), slra.ERR_INVALID_ARG), (dict(theta=0.5), slra.ERR_INVALID_ARG),
+    (dict(T=1 << 16, H=1 << 8, W=1 << 7), slra.ERR_INVALID_ARG), (dict(theta=1.0), slra.ERR_NO_DEVICE),
+    (dict(q_strides=(1 << 35, 64, 1 << 31)), slra.ERR_UNSUPPORTED), (dict(rope_split=(20, 10, 3)), slra.ERR_INVALID_ARG),
     (dict(rope_split=(-1, 10, 3)), slra.ERR_INVALID_ARG), (dict(rope_split=(10, 10, 3)), slra.ERR_NO_DEVICE),
     (dict(norm=3), slra.ERR_INVALID_ARG), (dict(rotate=2), slra.ERR_INVALID_ARG), (dict(pairing=2), slra.ERR_INVALID_ARG),
     (dict(schedule=-1), slra.ERR_INVALID_ARG), (dict(x_dtype=3), slra.ERR_INVALID_ARG),
