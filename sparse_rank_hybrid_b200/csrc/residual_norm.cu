@@ -73,13 +73,64 @@ struct Place {
     }
 };
 
-// Y: 0 without y, 1 with it, 2 with its own norm.  A block-wide team takes ROWS rows a step while they share a
-// modulation row: what a step costs besides its vectors (the loop, the ring, the barrier and the sums'
-// exchanges) is shared by them, and the coefficients in registers serve both.
-template <typename TS, typename TB, int V, int Y, bool WIDE, int ROWS>
+// Copies a worker's rows in order, one ahead of the arithmetic at a time: `copy` issues a row's copies, `next`
+// moves their pointers on, `wrap` from behind a sample's last token to the next sample.
+struct Feed {
+    int run, left, tokens;  // rows until the next sample or the end, rows behind them
+    __device__ Feed(int n, int l0, int per_sample) : tokens(per_sample) {
+        run = min(n, tokens - l0);
+        left = n - run;
+    }
+    template <class Copy, class Next, class Wrap>
+    __device__ __forceinline__ void row(Ring& ring, Copy copy, Next next, Wrap wrap) {
+        if (run > 0) {
+            copy();
+            next();
+            ring.filled();
+            if (--run == 0 && left > 0) {
+                wrap();
+                run = min(left, tokens);
+                left -= run;
+            }
+        }
+        async_commit();
+    }
+};
+
+// Calls begin(rows), row(valid) for each row, end(rows, done) for every run of a worker's rows within one
+// modulation row.  A block-wide team runs through without looking at the row's number; teams that share a
+// warp keep in step.
+template <bool WIDE, class Begin, class Row, class End>
+__device__ __forceinline__ void runs(const Place<WIDE>& at, int per, int first, Begin begin, Row row, End end) {
+    if constexpr (WIDE) {
+        for (int i = 0; i < at.n;) {
+            const int rows = min(per - first, at.n - i);
+            begin(rows, i + rows < at.n);
+            for (int k = 0; k < rows; ++k) row(true);
+            i += rows;
+            first = 0;
+            end(rows, i);
+        }
+    } else {
+        int rows = 0, left = 0;
+        for (int i = 0; i < at.longest; ++i) {
+            const bool valid = i < at.n;
+            if (valid && left == 0) {
+                rows = left = min(per - first, at.n - i);
+                first = 0;
+                begin(rows, i + rows < at.n);
+            }
+            row(valid);
+            if (valid && --left == 0) end(rows, i + 1);
+        }
+    }
+}
+
+// Y: 0 without y, 1 with it, 2 with its own norm.
+template <typename TS, typename TB, int V, int Y, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? fwd_threads(V) : 128) residual_norm_fwd_kernel(const __grid_constant__ ResidualNormArgs a) {
     constexpr bool SPLIT = sizeof(TS) == 4;
-    constexpr int UX = kUnits<TS>, ONE = UX + (Y ? kUnits<TB> : 0), U = ROWS * V * ONE;
+    constexpr int UX = kUnits<TS>, ONE = UX + (Y ? kUnits<TB> : 0), U = V * ONE;
     extern __shared__ uint4 shared[];
     __shared__ __align__(16) float scratch[kTeamScratch];
     const Place<WIDE> at(a);
@@ -94,45 +145,33 @@ __global__ void __launch_bounds__(WIDE ? fwd_threads(V) : 128) residual_norm_fwd
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         on[v] = at.t + v * at.size < a.channels / 8;
-        if (!on[v])
-            for (int r = 0; r < ROWS; ++r) ring.clear((r * V + v) * ONE, ONE);
+        if (!on[v]) ring.clear(v * ONE, ONE);
     }
     RowWalk<const TS> px(a.x, at.b0, at.l0, a.tokens);
     RowWalk<const TB> py(a.y, at.b0, at.l0, a.tokens);
     RowWalk<TS> pxo(a.x_out, at.b0, at.l0, a.tokens);
     RowWalk<TB> ph(a.h, at.b0, at.l0, a.tokens);
 
-    int lp = at.l0, left = at.n;  // token of the next row to copy, rows still to copy
+    Feed feed(at.n, at.l0, a.tokens);
     auto prefetch = [&]() {
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            if (left <= 0) break;
-            --left;
+        feed.row(ring, [&]() {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (!on[v]) continue;
-                ring.copy<SPLIT>((r * V + v) * ONE, px.at(0, c0 + v * step), gap);
-                if (Y) ring.copy<SPLIT>((r * V + v) * ONE + UX, py.at(0, c0 + v * step), gap);
+                ring.copy<SPLIT>(v * ONE, px.at(c0 + v * step), gap);
+                if (Y) ring.copy<SPLIT>(v * ONE + UX, py.at(c0 + v * step), gap);
             }
-            px.next();
-            if (Y) py.next();
-            if (++lp == a.tokens) {
-                lp = 0;
-                px.wrap();
-                if (Y) py.wrap();
-            }
-        }
-        ring.filled();
-        async_commit();
+        }, [&]() { px.next(), py.next(); }, [&]() { px.wrap(), py.wrap(); });
     };
     for (int s = 0; s < a.stages - 1; ++s) prefetch();
 
     Vec cg[V], ca[V], cb[V];  // gate wp, w (1 + scale), b (1 + scale) + shift
 #pragma unroll
     for (int v = 0; v < V; ++v) cg[v] = ca[v] = cb[v] = vec_of(0.f);
-    int b = at.b0, l = at.l0, f = at.l0 / a.per, group_left = 0;
+    int b = at.b0, l = at.l0, f = at.l0 / a.per;
 
-    auto modulation = [&]() {
+    auto begin = [&](int rows, bool more) {
+        const bool last = l + rows == a.tokens;  // the next modulation row is of another sample
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = c0 + v * step;
@@ -142,6 +181,7 @@ __global__ void __launch_bounds__(WIDE ? fwd_threads(V) : 128) residual_norm_fwd
                 const Vec g = load_any<SPLIT>(a.gate.p, b * a.gate.b + f * a.gate.f + c, a.mod_dtype, 1.f, gap);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) cg[v].f[e] = mul2(w.f[e], g.f[e]);
+                if (more) prefetch_mod<SPLIT>(a.gate, a.mod_dtype, last ? b + 1 : b, last ? 0 : f + 1, c, gap);
             }
             if (a.norm) {
                 const Vec sc = load_any<SPLIT>(a.scale.p, b * a.scale.b + f * a.scale.f + c, a.mod_dtype, 0.f, gap);
@@ -154,205 +194,133 @@ __global__ void __launch_bounds__(WIDE ? fwd_threads(V) : 128) residual_norm_fwd
                     ca[v].f[e] = mul2(w.f[e], up);
                     cb[v].f[e] = fma2(bias.f[e], up, sh.f[e]);
                 }
+                if (more) {
+                    prefetch_mod<SPLIT>(a.scale, a.mod_dtype, last ? b + 1 : b, last ? 0 : f + 1, c, gap);
+                    prefetch_mod<SPLIT>(a.shift, a.mod_dtype, last ? b + 1 : b, last ? 0 : f + 1, c, gap);
+                }
             }
         }
     };
-    // rows [r0, r0 + R) of the step
-    auto rows = [&](auto count, int r0, bool valid) {
-        constexpr int R = decltype(count)::value;
-        Vec o[R][V];
-        [[maybe_unused]] float ry[R];
-        if constexpr (Y == 2) {
+    auto row = [&](bool valid) {
+        prefetch();
+        ring_wait(a.stages);
+        Vec o[V], y[V];
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
+        for (int v = 0; v < V; ++v) {
+            o[v] = ring.read<TS>(v * ONE);
+            if constexpr (Y != 0) y[v] = ring.read<TB>(v * ONE + UX);
+        }
+        ring.done();
+        if constexpr (Y != 0) {
+            if constexpr (Y == 2) {
                 float2 acc = both(0.f);
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const Vec y = ring.read<TB>(((r0 + r) * V + v) * ONE + UX);
+                for (int v = 0; v < V; ++v)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc = fma2(y.f[e], y.f[e], acc);
-                }
-                ry[r] = fold(acc);
+                    for (int e = 0; e < 4; ++e) acc = fma2(y[v].f[e], y[v].f[e], acc);
+                float q[1] = {fold(acc)};
+                team.sum(q);
+                const float2 ry = both(rsqrtf(q[0] * inv + a.post_eps));
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[v].f[e] = mul2(y[v].f[e], ry);
             }
-            team.sum(ry);
-#pragma unroll
-            for (int r = 0; r < R; ++r) ry[r] = rsqrtf(ry[r] * inv + a.post_eps);
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                o[r][v] = ring.read<TS>(((r0 + r) * V + v) * ONE);
-                if constexpr (Y != 0) {
-                    Vec y = ring.read<TB>(((r0 + r) * V + v) * ONE + UX);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (Y == 2) y.f[e] = mul2(y.f[e], both(ry[r]));
-                        if (scaled) o[r][v].f[e] = mul2(o[r][v].f[e], both(a.rs));
-                        o[r][v].f[e] = fma2(cg[v].f[e], y.f[e], o[r][v].f[e]);
-                    }
-                    if (valid && on[v]) store_vec<TS, SPLIT>(pxo.at(r, c0 + v * step), o[r][v], gap);
+                for (int e = 0; e < 4; ++e) {
+                    if (scaled) o[v].f[e] = mul2(o[v].f[e], both(a.rs));
+                    o[v].f[e] = fma2(cg[v].f[e], y[v].f[e], o[v].f[e]);
                 }
+                if (valid && on[v]) store_vec<TS, SPLIT>(pxo.at(c0 + v * step), o[v], gap);
             }
+            if (valid) pxo.next();
+        }
         if (!a.norm) return;
-        float q[2 * R], m[R], rd[R];
+        float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            float2 s1 = both(0.f), s2 = both(0.f);
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s1 = add2(s1, o[v].f[e]);
+                s2 = fma2(o[v].f[e], o[v].f[e], s2);
+            }
+        float q[2] = {fold(s1), fold(s2)}, m, r;
+        team.sum(q);
+        const bool centre = row_moments(q[0], q[1], inv, a.eps, layer, m, r);
+        if (WIDE ? centre : __any_sync(0xffffffffu, centre)) {  // every team of a warp takes part in the sum
+            float c[1] = {0.f};
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    s1 = add2(s1, o[r][v].f[e]);
-                    s2 = fma2(o[r][v].f[e], o[r][v].f[e], s2);
+                    const float2 d = add2(o[v].f[e], both(-m));
+                    if (on[v]) c[0] += fold(mul2(d, d));
                 }
-            q[2 * r] = fold(s1), q[2 * r + 1] = fold(s2);
-        }
-        team.sum(q);
-        bool any = false, centre[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            centre[r] = row_moments(q[2 * r], q[2 * r + 1], inv, a.eps, layer, m[r], rd[r]);
-            any |= centre[r];
-        }
-        if (WIDE ? any : __any_sync(0xffffffffu, any)) {  // every team of a warp takes part in the sum
-            float c[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                c[r] = 0.f;
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 d = add2(o[r][v].f[e], both(-m[r]));
-                        if (on[v]) c[r] += fold(mul2(d, d));
-                    }
-            }
             team.sum(c);
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-                if (centre[r]) rd[r] = rsqrtf(c[r] * inv + a.eps);
+            if (centre) r = rsqrtf(c[0] * inv + a.eps);
         }
+        const float2 rr = both(r), mr = both(-m * r);
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int v = 0; v < V; ++v) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float2 rr = both(rd[r]), mr = both(-m[r] * rd[r]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[r][v].f[e] = fma2(fma2(o[r][v].f[e], rr, mr), ca[v].f[e], cb[v].f[e]);
-                if (valid && on[v]) store_vec<TB, SPLIT>(ph.at(r, c0 + v * step), o[r][v], gap);
-            }
+            for (int e = 0; e < 4; ++e) o[v].f[e] = fma2(fma2(o[v].f[e], rr, mr), ca[v].f[e], cb[v].f[e]);
+            if (valid && on[v]) store_vec<TB, SPLIT>(ph.at(c0 + v * step), o[v], gap);
+        }
+        if (valid) ph.next();
     };
-    // moves on by R rows, which end at a modulation row's end at the latest
-    auto advance = [&](int R) {
-        l += R;
-        group_left -= R;
-        if (Y) pxo.next(R);
-        ph.next(R);
-        if (group_left == 0) {
-            ++f;
-            if (l == a.tokens) {
-                l = f = 0;
-                ++b;
-                if (Y) pxo.wrap();
-                ph.wrap();
-            }
+    auto end = [&](int rows, int) {
+        l += rows;
+        ++f;
+        if (l == a.tokens) {
+            l = f = 0;
+            ++b;
+            pxo.wrap(), ph.wrap();
         }
     };
-
-    for (int i = 0; i < at.longest; i += ROWS) {
-        prefetch();
-        ring_wait(a.stages);
-        const int rest = at.n - i;  // rows of this step and behind it
-        if (WIDE && ROWS > 1 && rest >= ROWS && group_left >= ROWS) {
-            rows(Count<ROWS>{}, 0, true);
-            advance(ROWS);
-        } else {
-#pragma unroll 1
-            for (int r = 0; r < ROWS; ++r) {
-                const bool valid = r < rest;
-                if (WIDE && !valid) break;
-                if (valid && group_left == 0) {
-                    modulation();
-                    group_left = a.per - (l - f * a.per);
-                }
-                if (valid && group_left == 1 && rest > r + 1) {  // the next row has another modulation row
-                    const bool wrap = l + 1 == a.tokens;
-                    const int nb = wrap ? b + 1 : b, nf = wrap ? 0 : f + 1;
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const int c = c0 + v * step;
-                        if (!on[v]) continue;
-                        if (Y) prefetch_mod<SPLIT>(a.gate, a.mod_dtype, nb, nf, c, gap);
-                        prefetch_mod<SPLIT>(a.scale, a.mod_dtype, nb, nf, c, gap);
-                        prefetch_mod<SPLIT>(a.shift, a.mod_dtype, nb, nf, c, gap);
-                    }
-                }
-                rows(Count<1>{}, r, valid);
-                if (valid) advance(1);
-            }
-        }
-        ring.done();
-    }
+    runs<WIDE>(at, a.per, l - f * a.per, begin, row, end);
 }
 
-template <typename TS, typename TB, int V, int Y, bool WIDE, int ROWS>
+template <typename TS, typename TB, int V, int Y, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? bwd_threads(V) : 128) residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a) {
     constexpr bool SPLIT = sizeof(TS) == 4;
     constexpr int UX = kUnits<TS>, UB = kUnits<TB>;
     // x, dx_out, dh and y of each vector
-    constexpr int DXO = UX, DH = 2 * UX, YU = 2 * UX + UB, ONE = 2 * UX + (Y ? 2 : 1) * UB, U = ROWS * V * ONE;
+    constexpr int DXO = UX, DH = 2 * UX, YU = 2 * UX + UB, ONE = 2 * UX + (Y ? 2 : 1) * UB, U = V * ONE;
     extern __shared__ uint4 shared[];
     __shared__ __align__(16) float scratch[kTeamScratch];
     const Place<WIDE> at(a);
     Team<WIDE> team(at.size, scratch);
     const int c0 = at.t * (SPLIT ? 4 : 8), step = at.size * (SPLIT ? 4 : 8), gap = SPLIT ? a.channels / 2 : 4;
     const float inv = 1.0f / a.channels;
-    const bool layer = a.norm == kNormLayer, has_dxo = a.dx_out.p != nullptr, has_dh = a.norm != kNormNone;
-    const bool scaled = a.rs != 1.f;
+    const bool layer = a.norm == kNormLayer, scaled = a.rs != 1.f;
+    const bool has_dxo = a.dx_out.p != nullptr, has_dh = a.norm != kNormNone;
 
     Ring ring(shared_address(shared), a.stages, U);
     bool on[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         on[v] = at.t + v * at.size < a.channels / 8;
-        if (!on[v])
-            for (int r = 0; r < ROWS; ++r) ring.clear((r * V + v) * ONE, ONE);
+        if (!on[v]) ring.clear(v * ONE, ONE);
     }
     RowWalk<const TS> px(a.x, at.b0, at.l0, a.tokens), pdo(a.dx_out, at.b0, at.l0, a.tokens);
     RowWalk<const TB> py(a.y, at.b0, at.l0, a.tokens), pdh(a.dh, at.b0, at.l0, a.tokens);
     RowWalk<TS> pdx(a.dx, at.b0, at.l0, a.tokens);
     RowWalk<TB> pdy(a.dy, at.b0, at.l0, a.tokens);
 
-    int lp = at.l0, left = at.n;
+    Feed feed(at.n, at.l0, a.tokens);
     auto prefetch = [&]() {
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            if (left <= 0) break;
-            --left;
+        feed.row(ring, [&]() {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (!on[v]) continue;
-                const int u = (r * V + v) * ONE;
-                ring.copy<SPLIT>(u, px.at(0, c0 + v * step), gap);
-                if (has_dxo) ring.copy<SPLIT>(u + DXO, pdo.at(0, c0 + v * step), gap);
-                if (has_dh) ring.copy<SPLIT>(u + DH, pdh.at(0, c0 + v * step), gap);
-                if (Y) ring.copy<SPLIT>(u + YU, py.at(0, c0 + v * step), gap);
+                ring.copy<SPLIT>(v * ONE, px.at(c0 + v * step), gap);
+                if (has_dxo) ring.copy<SPLIT>(v * ONE + DXO, pdo.at(c0 + v * step), gap);
+                if (has_dh) ring.copy<SPLIT>(v * ONE + DH, pdh.at(c0 + v * step), gap);
+                if (Y) ring.copy<SPLIT>(v * ONE + YU, py.at(c0 + v * step), gap);
             }
-            px.next();
-            pdo.next();
-            pdh.next();
-            if (Y) py.next();
-            if (++lp == a.tokens) {
-                lp = 0;
-                px.wrap();
-                pdo.wrap();
-                pdh.wrap();
-                if (Y) py.wrap();
-            }
-        }
-        ring.filled();
-        async_commit();
+        }, [&]() { px.next(), pdo.next(), pdh.next(), py.next(); }, [&]() { px.wrap(), pdo.wrap(), pdh.wrap(), py.wrap(); });
     };
     for (int s = 0; s < a.stages - 1; ++s) prefetch();
 
@@ -380,8 +348,9 @@ __global__ void __launch_bounds__(WIDE ? bwd_threads(V) : 128) residual_norm_bwd
         w[we] += d.y;
     };
 
-    int b = at.b0, l = at.l0, f = at.l0 / a.per, group_left = 0, seg_rows = 0;
-    auto modulation = [&]() {
+    int b = at.b0, l = at.l0, f = at.l0 / a.per;
+    auto begin = [&](int rows, bool more) {
+        const bool last = l + rows == a.tokens;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = c0 + v * step;
@@ -391,164 +360,139 @@ __global__ void __launch_bounds__(WIDE ? bwd_threads(V) : 128) residual_norm_bwd
                 const Vec g = load_any<SPLIT>(a.gate.p, b * a.gate.b + f * a.gate.f + c, a.mod_dtype, 1.f, gap);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) cg[v].f[e] = mul2(w.f[e], g.f[e]);
+                if (more) prefetch_mod<SPLIT>(a.gate, a.mod_dtype, last ? b + 1 : b, last ? 0 : f + 1, c, gap);
             }
             const Vec w = load_any<SPLIT>(a.weight, c, a.w_dtype, 1.f, gap);
             const Vec sc = load_any<SPLIT>(a.scale.p, b * a.scale.b + f * a.scale.f + c, a.mod_dtype, 0.f, gap);
 #pragma unroll
             for (int e = 0; e < 4; ++e) ca[v].f[e] = fma2(w.f[e], sc.f[e], w.f[e]);
+            if (more) prefetch_mod<SPLIT>(a.scale, a.mod_dtype, last ? b + 1 : b, last ? 0 : f + 1, c, gap);
         }
     };
-    // Rows [r0, r0 + R) of the step.  Of a row only o stays in registers across a sum; the rest is read again
-    // from the ring where it is needed, which costs less than the registers to keep it.
-    auto rows = [&](auto count, int r0, bool valid) {
-        constexpr int R = decltype(count)::value;
-        Vec o[R][V];  // rs x + gate wp yh, then t, the gradient that reaches it
-        [[maybe_unused]] float ry[R];
+    // Of a row only o stays in registers across a sum; the rest is read again from the ring where it is
+    // needed, which costs less than the registers to keep it.
+    auto row = [&](bool valid) {
+        prefetch();
+        ring_wait(a.stages);
+        Vec o[V];  // rs x + gate wp yh, then t, the gradient that reaches it
+        float2 ry = both(1.f);
         if constexpr (Y == 2) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                float2 acc = both(0.f);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const Vec y = ring.read<TB>(((r0 + r) * V + v) * ONE + YU);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc = fma2(y.f[e], y.f[e], acc);
-                }
-                ry[r] = fold(acc);
-            }
-            team.sum(ry);
-#pragma unroll
-            for (int r = 0; r < R; ++r) ry[r] = rsqrtf(ry[r] * inv + a.post_eps);
-        }
-        float rd[R], mr[R], k1[R], k0[R];
-        if (has_dh) {
-            float q[4 * R], m[R], am[R], an[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                float2 s1 = both(0.f), s2 = both(0.f), s3 = both(0.f), s4 = both(0.f);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const int u = ((r0 + r) * V + v) * ONE;
-                    o[r][v] = ring.read<TS>(u);
-                    if constexpr (Y != 0) {
-                        Vec y = ring.read<TB>(u + YU);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (Y == 2) y.f[e] = mul2(y.f[e], both(ry[r]));
-                            if (scaled) o[r][v].f[e] = mul2(o[r][v].f[e], both(a.rs));
-                            o[r][v].f[e] = fma2(cg[v].f[e], y.f[e], o[r][v].f[e]);
-                        }
-                    }
-                    const Vec dh = ring.read<TB>(u + DH);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 d = mul2(dh.f[e], ca[v].f[e]);
-                        s1 = add2(s1, o[r][v].f[e]);
-                        s2 = fma2(o[r][v].f[e], o[r][v].f[e], s2);
-                        s3 = add2(s3, d);
-                        s4 = fma2(o[r][v].f[e], d, s4);
-                    }
-                }
-                q[4 * r] = fold(s1), q[4 * r + 1] = fold(s2), q[4 * r + 2] = fold(s3), q[4 * r + 3] = fold(s4);
-            }
-            team.sum(q);
-            bool any = false, centre[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                centre[r] = row_moments(q[4 * r], q[4 * r + 1], inv, a.eps, layer, m[r], rd[r]);
-                any |= centre[r];
-                am[r] = layer ? q[4 * r + 2] * inv : 0.f;
-                an[r] = fmaf(-m[r], q[4 * r + 2], q[4 * r + 3]);  // sum of a (o - m)
-            }
-            if (WIDE ? any : __any_sync(0xffffffffu, any)) {
-                float c[2 * R];
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    c[2 * r] = c[2 * r + 1] = 0.f;
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        if (!on[v]) continue;
-                        const Vec dh = ring.read<TB>(((r0 + r) * V + v) * ONE + DH);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 d = add2(o[r][v].f[e], both(-m[r]));
-                            c[2 * r] += fold(mul2(d, d));
-                            c[2 * r + 1] += fold(mul2(d, mul2(dh.f[e], ca[v].f[e])));
-                        }
-                    }
-                }
-                team.sum(c);
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-                    if (centre[r]) rd[r] = rsqrtf(c[2 * r] * inv + a.eps), an[r] = c[2 * r + 1];
-            }
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                // with n = o rd + mr: rd (a - am - n mean(a n)) = rd a + k1 o + k0
-                const float mean_an = an[r] * rd[r] * inv;
-                mr[r] = -m[r] * rd[r];
-                k1[r] = -rd[r] * rd[r] * mean_an;
-                k0[r] = -rd[r] * fmaf(mr[r], mean_an, am[r]);
-            }
-        }
-        float su[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
             float2 acc = both(0.f);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const int u = ((r0 + r) * V + v) * ONE;
-                Vec d = has_dxo ? ring.read<TS>(u + DXO) : vec_of(0.f);
-                if (has_dh) {
-                    const Vec dh = ring.read<TB>(u + DH);
+                const Vec y = ring.read<TB>(v * ONE + YU);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (valid) {
-                            p0[v].f[e] = add2(p0[v].f[e], dh.f[e]);
-                            p1[v].f[e] = fma2(dh.f[e], fma2(o[r][v].f[e], both(rd[r]), both(mr[r])), p1[v].f[e]);
-                        }
-                        d.f[e] = add2(d.f[e], fma2(o[r][v].f[e], both(k1[r]), both(k0[r])));
-                        o[r][v].f[e] = fma2(mul2(dh.f[e], ca[v].f[e]), both(rd[r]), d.f[e]);
-                    }
-                } else {
-                    o[r][v] = d;
-                }
+                for (int e = 0; e < 4; ++e) acc = fma2(y.f[e], y.f[e], acc);
+            }
+            float q[1] = {fold(acc)};
+            team.sum(q);
+            ry = both(rsqrtf(q[0] * inv + a.post_eps));
+        }
+        float rd = 0.f, mr = 0.f, k1 = 0.f, k0 = 0.f;
+        if (has_dh) {
+            float2 s1 = both(0.f), s2 = both(0.f), s3 = both(0.f), s4 = both(0.f);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) d.f[e] = scaled ? mul2(both(a.rs), o[r][v].f[e]) : o[r][v].f[e];
-                if (valid && on[v]) store_vec<TS, SPLIT>(pdx.at(r, c0 + v * step), d, gap);
+            for (int v = 0; v < V; ++v) {
+                o[v] = ring.read<TS>(v * ONE);
                 if constexpr (Y != 0) {
-                    Vec y = ring.read<TB>(u + YU);
+                    Vec y = ring.read<TB>(v * ONE + YU);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        if (Y == 2) y.f[e] = mul2(y.f[e], both(ry[r]));
-                        if (valid) pq[v].f[e] = fma2(o[r][v].f[e], y.f[e], pq[v].f[e]);
-                        o[r][v].f[e] = mul2(o[r][v].f[e], cg[v].f[e]);
-                        if (Y == 2) acc = fma2(o[r][v].f[e], y.f[e], acc);
+                        if (Y == 2) y.f[e] = mul2(y.f[e], ry);
+                        if (scaled) o[v].f[e] = mul2(o[v].f[e], both(a.rs));
+                        o[v].f[e] = fma2(cg[v].f[e], y.f[e], o[v].f[e]);
                     }
-                    if (Y == 1 && valid && on[v]) store_vec<TB, SPLIT>(pdy.at(r, c0 + v * step), o[r][v], gap);
+                }
+                const Vec dh = ring.read<TB>(v * ONE + DH);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 d = mul2(dh.f[e], ca[v].f[e]);
+                    s1 = add2(s1, o[v].f[e]);
+                    s2 = fma2(o[v].f[e], o[v].f[e], s2);
+                    s3 = add2(s3, d);
+                    s4 = fma2(o[v].f[e], d, s4);
                 }
             }
-            su[r] = fold(acc);
-        }
-        if constexpr (Y == 2) {
-            team.sum(su);
-#pragma unroll
-            for (int r = 0; r < R; ++r)
+            float q[4] = {fold(s1), fold(s2), fold(s3), fold(s4)}, m;
+            team.sum(q);
+            const bool centre = row_moments(q[0], q[1], inv, a.eps, layer, m, rd);
+            const float am = layer ? q[2] * inv : 0.f;
+            float an = fmaf(-m, q[2], q[3]);  // sum of a (o - m)
+            if (WIDE ? centre : __any_sync(0xffffffffu, centre)) {
+                float c[2] = {0.f, 0.f};
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    const Vec y = ring.read<TB>(((r0 + r) * V + v) * ONE + YU);
-                    const float2 mu = both(-su[r] * inv * ry[r]);
+                    if (!on[v]) continue;
+                    const Vec dh = ring.read<TB>(v * ONE + DH);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[r][v].f[e] = mul2(both(ry[r]), fma2(y.f[e], mu, o[r][v].f[e]));
-                    if (valid && on[v]) store_vec<TB, SPLIT>(pdy.at(r, c0 + v * step), o[r][v], gap);
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 d = add2(o[v].f[e], both(-m));
+                        c[0] += fold(mul2(d, d));
+                        c[1] += fold(mul2(d, mul2(dh.f[e], ca[v].f[e])));
+                    }
                 }
+                team.sum(c);
+                if (centre) rd = rsqrtf(c[0] * inv + a.eps), an = c[1];
+            }
+            // with n = o rd + mr: rd (a - am - n mean(a n)) = rd a + k1 o + k0
+            an *= rd * inv;
+            mr = -m * rd;
+            k1 = -rd * rd * an;
+            k0 = -rd * fmaf(mr, an, am);
         }
+        float2 su = both(0.f);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            Vec d = has_dxo ? ring.read<TS>(v * ONE + DXO) : vec_of(0.f);
+            if (has_dh) {
+                const Vec dh = ring.read<TB>(v * ONE + DH);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (valid) {
+                        p0[v].f[e] = add2(p0[v].f[e], dh.f[e]);
+                        p1[v].f[e] = fma2(dh.f[e], fma2(o[v].f[e], both(rd), both(mr)), p1[v].f[e]);
+                    }
+                    d.f[e] = add2(d.f[e], fma2(o[v].f[e], both(k1), both(k0)));
+                    o[v].f[e] = fma2(mul2(dh.f[e], ca[v].f[e]), both(rd), d.f[e]);
+                }
+            } else {
+                o[v] = d;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d.f[e] = scaled ? mul2(both(a.rs), o[v].f[e]) : o[v].f[e];
+            if (valid && on[v]) store_vec<TS, SPLIT>(pdx.at(c0 + v * step), d, gap);
+            if constexpr (Y != 0) {
+                Vec y = ring.read<TB>(v * ONE + YU);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (Y == 2) y.f[e] = mul2(y.f[e], ry);
+                    if (valid) pq[v].f[e] = fma2(o[v].f[e], y.f[e], pq[v].f[e]);
+                    o[v].f[e] = mul2(o[v].f[e], cg[v].f[e]);
+                    if (Y == 2) su = fma2(o[v].f[e], y.f[e], su);
+                }
+                if (Y == 1 && valid && on[v]) store_vec<TB, SPLIT>(pdy.at(c0 + v * step), o[v], gap);
+            }
+        }
+        if constexpr (Y == 2) {
+            float q[1] = {fold(su)};
+            team.sum(q);
+            const float2 mu = both(-q[0] * inv * ry.x);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const Vec y = ring.read<TB>(v * ONE + YU);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[v].f[e] = mul2(ry, fma2(y.f[e], mu, o[v].f[e]));
+                if (valid && on[v]) store_vec<TB, SPLIT>(pdy.at(c0 + v * step), o[v], gap);
+            }
+        }
+        ring.done();
+        if (valid) pdx.next(), pdy.next();
     };
-    // The end of the modulation row, or of this worker's part of it (`ended` of its rows done): the sums go
+    // The end of the modulation row, or of this worker's part of it (`done` of its rows so far): the sums go
     // straight to the gradients where the worker had all its rows, else to the worker's first or last slot.
-    auto flush = [&](int ended) {
-        const bool whole = seg_rows == a.per;
-        const long long slot = 2ll * at.worker + (ended != seg_rows ? 1 : 0);
+    auto end = [&](int rows, int done) {
+        const bool whole = rows == a.per;
+        const long long slot = 2ll * at.worker + (done != rows ? 1 : 0);
         const long long g = (static_cast<long long>(b) * a.groups + f) * a.channels;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -589,59 +533,15 @@ __global__ void __launch_bounds__(WIDE ? bwd_threads(V) : 128) residual_norm_bwd
             }
             p0[v] = p1[v] = pq[v] = vec_of(0.f);
         }
-        seg_rows = 0;
-    };
-    auto advance = [&](int R, int ended) {
-        seg_rows += R;
-        group_left -= R;
-        if (group_left == 0 || ended == at.n) flush(ended);
-        l += R;
-        pdx.next(R);
-        if (Y) pdy.next(R);
-        if (group_left == 0) {
-            ++f;
-            if (l == a.tokens) {
-                l = f = 0;
-                ++b;
-                pdx.wrap();
-                if (Y) pdy.wrap();
-            }
+        l += rows;
+        ++f;
+        if (l == a.tokens) {
+            l = f = 0;
+            ++b;
+            pdx.wrap(), pdy.wrap();
         }
     };
-
-    for (int i = 0; i < at.longest; i += ROWS) {
-        prefetch();
-        ring_wait(a.stages);
-        const int rest = at.n - i;
-        if (WIDE && ROWS > 1 && rest >= ROWS && group_left >= ROWS) {
-            rows(Count<ROWS>{}, 0, true);
-            advance(ROWS, i + ROWS);
-        } else {
-#pragma unroll 1
-            for (int r = 0; r < ROWS; ++r) {
-                const bool valid = r < rest;
-                if (WIDE && !valid) break;
-                if (valid && group_left == 0) {
-                    modulation();
-                    group_left = a.per - (l - f * a.per);
-                }
-                if (valid && group_left == 1 && rest > r + 1) {
-                    const bool wrap = l + 1 == a.tokens;
-                    const int nb = wrap ? b + 1 : b, nf = wrap ? 0 : f + 1;
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const int c = c0 + v * step;
-                        if (!on[v]) continue;
-                        if (Y) prefetch_mod<SPLIT>(a.gate, a.mod_dtype, nb, nf, c, gap);
-                        prefetch_mod<SPLIT>(a.scale, a.mod_dtype, nb, nf, c, gap);
-                    }
-                }
-                rows(Count<1>{}, r, valid);
-                if (valid) advance(1, i + r + 1);
-            }
-        }
-        ring.done();
-    }
+    runs<WIDE>(at, a.per, l - f * a.per, begin, row, end);
     if (a.wpart && a.wsum_shared)
         for (int v = 0; v < V && on[v]; ++v)
             for (int k = 0; k < 3; ++k)
@@ -729,7 +629,7 @@ __global__ void __launch_bounds__(32 * kFinalWarps) residual_norm_final_kernel(c
 
 // Blocks that a processor holds at once, from the registers the kernels need.
 int blocks_per_sm(const RowPlan& p, bool backward) {
-    const int threads = backward ? bwd_threads(p.V) : p.V == 1 ? 1024 : 640;
+    const int threads = backward ? bwd_threads(p.V) : p.V == 1 ? 1024 : 640;  // 96 or 128 registers; 64 or 96
     return std::max(1, threads / p.threads);
 }
 
@@ -744,23 +644,18 @@ cudaError_t launch(K kernel, const ResidualNormArgs& a, const RowPlan& p, size_t
     return cudaGetLastError();
 }
 
-// The backward takes two rows a step where the ring holds two such steps.
 template <typename TS, typename TB, int V, int Y, bool WIDE>
 cudaError_t launch_dir(ResidualNormArgs a, const RowPlan& p, bool backward, cudaStream_t st) {
     const int units = backward ? 2 * kUnits<TS> + (Y ? 2 : 1) * kUnits<TB> : kUnits<TS> + (Y ? kUnits<TB> : 0);
-    const size_t row = size_t(16) * V * units * p.threads, sums = size_t(3) * V * 32 * p.threads;
+    const size_t stage = size_t(16) * V * units * p.threads, sums = size_t(3) * V * 32 * p.threads;
     const int per_sm = blocks_per_sm(p, backward);
     const size_t room = kRingBytes / per_sm;
-    const int rows = WIDE && backward && 4 * row <= room ? 2 : 1;
-    a.stages = ring_stages(rows * row, per_sm, room, (a.rows + a.workers - 1) / a.workers, rows);
+    a.stages = ring_stages(stage, per_sm, room, (a.rows + a.workers - 1) / a.workers, 1);
     // the weights' sums take what the ring leaves
-    a.wsum_shared = backward && a.wpart && a.stages * rows * row + sums <= room;
-    const size_t smem = a.stages * rows * row + (a.wsum_shared ? sums : 0);
-    if (!backward) return launch(residual_norm_fwd_kernel<TS, TB, V, Y, WIDE, 1>, a, p, smem, st);
-    if constexpr (WIDE) {
-        if (rows == 2) return launch(residual_norm_bwd_kernel<TS, TB, V, Y, WIDE, 2>, a, p, smem, st);
-    }
-    return launch(residual_norm_bwd_kernel<TS, TB, V, Y, WIDE, 1>, a, p, smem, st);
+    a.wsum_shared = backward && a.wpart && a.stages * stage + sums <= room;
+    const size_t smem = a.stages * stage + (a.wsum_shared ? sums : 0);
+    return backward ? launch(residual_norm_bwd_kernel<TS, TB, V, Y, WIDE>, a, p, smem, st)
+                    : launch(residual_norm_fwd_kernel<TS, TB, V, Y, WIDE>, a, p, smem, st);
 }
 template <typename TS, typename TB, int V, bool WIDE>
 cudaError_t launch_y(const ResidualNormArgs& a, const RowPlan& p, bool backward, cudaStream_t st) {
@@ -782,7 +677,7 @@ cudaError_t launch_types(const ResidualNormArgs& a, const RowPlan& p, bool backw
 RowPlan residual_norm_plan(long long rows, int channels, bool backward) {
     RowPlan p;
     const int slots = channels / 8;
-    row_team(slots, slots > (backward ? bwd_threads(1) : 384) ? 2 : 1, &p);
+    row_team(slots, slots > 640 ? 2 : 1, &p);
     row_workers(rows, kSMs * blocks_per_sm(p, backward), &p);
     return p;
 }

@@ -227,12 +227,6 @@ __device__ __forceinline__ void ring_wait(int stages) {
 }
 constexpr int kMaxStages = 4;
 
-// A compile-time count as an argument.
-template <int N>
-struct Count {
-    static constexpr int value = N;
-};
-
 // A team of threads shares a row: the whole block (WIDE; a multiple of 32 threads, at most 1024), or
 // `size` threads of a warp, a power of two (then several teams in a block).
 constexpr int kTeamScratch = 2 * 8 * 32;  // floats of shared memory for a block-wide team's sums
@@ -322,11 +316,10 @@ struct RowWalk {
           step(sl * static_cast<int>(sizeof(T))),
           back((sb - tokens * sl) * static_cast<int>(sizeof(T))) {}
     __device__ RowWalk(const RowTensor& t, int b, int l, int tokens) : RowWalk(t.p, t.b, t.l, b, l, tokens) {}
-    // element c of the row `r` rows on
-    __device__ __forceinline__ T* at(int r, int c) const {
-        return reinterpret_cast<T*>(p + r * step + static_cast<unsigned>(c * static_cast<int>(sizeof(T))));
+    __device__ __forceinline__ T* at(int c) const {  // element c
+        return reinterpret_cast<T*>(p + static_cast<unsigned>(c * static_cast<int>(sizeof(T))));
     }
-    __device__ __forceinline__ void next(int rows = 1) { p += rows * step; }
+    __device__ __forceinline__ void next() { p += step; }
     __device__ __forceinline__ void wrap() { p += back; }
 };
 
