@@ -114,32 +114,30 @@ __global__ void __launch_bounds__(WIDE ? rope_threads(VQ + VK, BWD) : 128)
     const RopeSide& sq = a.side[side_q];
     const RopeSide& sk = a.side[1];
 
-    int lp = l0, left = n;  // token of the next row to copy, rows still to copy
+    Feed feed(n, l0, a.tokens);
     auto prefetch = [&]() {
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            if (left <= 0) break;
-            --left;
+        for (int r = 0; r < R; ++r)
+            feed.row([&]() {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (need_x) {
-                    if (on[v]) ring.copy<SPLIT>((r * V + v) * ONE, reinterpret_cast<const TX*>(px[v]), gap);
+                for (int v = 0; v < V; ++v) {
+                    if (!on[v]) continue;
+                    if (need_x) ring.copy<SPLIT>((r * V + v) * ONE, reinterpret_cast<const TX*>(px[v]), gap);
+                    if (BWD) ring.copy<SPLIT>((r * V + v) * ONE + UX, reinterpret_cast<const TO*>(pd[v]), gap);
+                }
+            }, [&]() {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
                     px[v] += v < VQ ? sq.next_x : sk.next_x;
+                    if (BWD) pd[v] += v < VQ ? sq.next_d : sk.next_d;
                 }
-                if (BWD) {
-                    if (on[v]) ring.copy<SPLIT>((r * V + v) * ONE + UX, reinterpret_cast<const TO*>(pd[v]), gap);
-                    pd[v] += v < VQ ? sq.next_d : sk.next_d;
-                }
-            }
-            if (++lp == a.tokens) {
-                lp = 0;
+            }, [&]() {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     px[v] += v < VQ ? sq.wrap_x : sk.wrap_x;
                     if (BWD) pd[v] += v < VQ ? sq.wrap_d : sk.wrap_d;
                 }
-            }
-        }
+            });
         ring.filled();
         async_commit();
     };
@@ -179,7 +177,8 @@ __global__ void __launch_bounds__(WIDE ? rope_threads(VQ + VK, BWD) : 128)
     const float inv_q = 1.0f / (static_cast<float>(D) * a.side[side_q].heads);
     const float inv_k = 1.0f / (static_cast<float>(D) * max(1, a.side[1].heads));
     const bool has_pairs = lane * 8 < D;
-    int l = l0, which = 0;
+    Feed store(n, l0, a.tokens);
+    int which = 0;
     for (int i = 0; i < longest; i += R) {
         prefetch();
         float2 c[R][2], sn[R][2];
@@ -274,35 +273,36 @@ __global__ void __launch_bounds__(WIDE ? rope_threads(VQ + VK, BWD) : 128)
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const bool row = i + r < n;
+            store.row([&]() {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                TW* out = reinterpret_cast<TW*>(po[v]);
-                po[v] += v < VQ ? sq.next_o : sk.next_o;
-                if (!BWD) {
-                    if (a.norm)
+                for (int v = 0; v < V; ++v) {
+                    TW* out = reinterpret_cast<TW*>(po[v]);
+                    if (!BWD) {
+                        if (a.norm)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            x[r][v].f[e] = mul2(x[r][v].f[e], mul2(w[v].f[e], both(rd[r][v])));
-                    if (a.rotate) rotate<SPLIT>(x[r][v], c[r], sn[r]);
-                    if (row && on[v]) store_vec<TW, SPLIT>(out, x[r][v], gap);
-                } else {
-                    if (a.norm) {
-                        const float2 rr = both(rd[r][v]), mg = both(-gx[r][v]);
+                            for (int e = 0; e < 4; ++e)
+                                x[r][v].f[e] = mul2(x[r][v].f[e], mul2(w[v].f[e], both(rd[r][v])));
+                        if (a.rotate) rotate<SPLIT>(x[r][v], c[r], sn[r]);
+                        if (on[v]) store_vec<TW, SPLIT>(out, x[r][v], gap);
+                    } else {
+                        if (a.norm) {
+                            const float2 rr = both(rd[r][v]), mg = both(-gx[r][v]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (row) dw[v].f[e] = fma2(g[r][v].f[e], mul2(x[r][v].f[e], rr), dw[v].f[e]);
-                            g[r][v].f[e] = mul2(rr, fma2(x[r][v].f[e], mg, mul2(g[r][v].f[e], w[v].f[e])));
+                            for (int e = 0; e < 4; ++e) {
+                                dw[v].f[e] = fma2(g[r][v].f[e], mul2(x[r][v].f[e], rr), dw[v].f[e]);
+                                g[r][v].f[e] = mul2(rr, fma2(x[r][v].f[e], mg, mul2(g[r][v].f[e], w[v].f[e])));
+                            }
                         }
+                        if (on[v]) store_vec<TW, SPLIT>(out, g[r][v], gap);
                     }
-                    if (row && on[v]) store_vec<TW, SPLIT>(out, g[r][v], gap);
                 }
-            }
-            if (++l == a.tokens) {
-                l = 0;
+            }, [&]() {
+#pragma unroll
+                for (int v = 0; v < V; ++v) po[v] += v < VQ ? sq.next_o : sk.next_o;
+            }, [&]() {
 #pragma unroll
                 for (int v = 0; v < V; ++v) po[v] += v < VQ ? sq.wrap_o : sk.wrap_o;
-            }
+            });
         }
     }
 

@@ -73,30 +73,6 @@ struct Place {
     }
 };
 
-// Copies a worker's rows in order, one ahead of the arithmetic at a time: `copy` issues a row's copies, `next`
-// moves their pointers on, `wrap` from behind a sample's last token to the next sample.
-struct Feed {
-    int run, left, tokens;  // rows until the next sample or the end, rows behind them
-    __device__ Feed(int n, int l0, int per_sample) : tokens(per_sample) {
-        run = min(n, tokens - l0);
-        left = n - run;
-    }
-    template <class Copy, class Next, class Wrap>
-    __device__ __forceinline__ void row(Ring& ring, Copy copy, Next next, Wrap wrap) {
-        if (run > 0) {
-            copy();
-            next();
-            ring.filled();
-            if (--run == 0 && left > 0) {
-                wrap();
-                run = min(left, tokens);
-                left -= run;
-            }
-        }
-        async_commit();
-    }
-};
-
 // Calls begin(rows), row(valid) for each row, end(rows, done) for every run of a worker's rows within one
 // modulation row.  A block-wide team runs through without looking at the row's number; teams that share a
 // warp keep in step.
@@ -154,7 +130,7 @@ __global__ void __launch_bounds__(WIDE ? fwd_threads(V) : 128) residual_norm_fwd
 
     Feed feed(at.n, at.l0, a.tokens);
     auto prefetch = [&]() {
-        feed.row(ring, [&]() {
+        feed.row([&]() {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (!on[v]) continue;
@@ -162,6 +138,8 @@ __global__ void __launch_bounds__(WIDE ? fwd_threads(V) : 128) residual_norm_fwd
                 if (Y) ring.copy<SPLIT>(v * ONE + UX, py.at(c0 + v * step), gap);
             }
         }, [&]() { px.next(), py.next(); }, [&]() { px.wrap(), py.wrap(); });
+        ring.filled();
+        async_commit();
     };
     for (int s = 0; s < a.stages - 1; ++s) prefetch();
 
@@ -311,7 +289,7 @@ __global__ void __launch_bounds__(WIDE ? bwd_threads(V) : 128) residual_norm_bwd
 
     Feed feed(at.n, at.l0, a.tokens);
     auto prefetch = [&]() {
-        feed.row(ring, [&]() {
+        feed.row([&]() {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (!on[v]) continue;
@@ -321,6 +299,8 @@ __global__ void __launch_bounds__(WIDE ? bwd_threads(V) : 128) residual_norm_bwd
                 if (Y) ring.copy<SPLIT>(v * ONE + YU, py.at(c0 + v * step), gap);
             }
         }, [&]() { px.next(), pdo.next(), pdh.next(), py.next(); }, [&]() { px.wrap(), pdo.wrap(), pdh.wrap(), py.wrap(); });
+        ring.filled();
+        async_commit();
     };
     for (int s = 0; s < a.stages - 1; ++s) prefetch();
 

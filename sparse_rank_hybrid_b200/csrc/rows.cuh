@@ -227,6 +227,28 @@ __device__ __forceinline__ void ring_wait(int stages) {
 }
 constexpr int kMaxStages = 4;
 
+// A worker's rows in order: `each` for a row while there are any, `next` moves pointers on to the following
+// one, `wrap` from behind a sample's last token to the next sample.
+struct Feed {
+    int run, left, tokens;  // rows until the next sample or the end, rows behind them
+    __device__ Feed(int n, int l0, int per_sample) : tokens(per_sample) {
+        run = min(n, tokens - l0);
+        left = n - run;
+    }
+    template <class Each, class Next, class Wrap>
+    __device__ __forceinline__ void row(Each each, Next next, Wrap wrap) {
+        if (run > 0) {
+            each();
+            next();
+            if (--run == 0 && left > 0) {
+                wrap();
+                run = min(left, tokens);
+                left -= run;
+            }
+        }
+    }
+};
+
 // A team of threads shares a row: the whole block (WIDE; a multiple of 32 threads, at most 1024), or
 // `size` threads of a warp, a power of two (then several teams in a block).
 constexpr int kTeamScratch = 2 * 8 * 32;  // floats of shared memory for a block-wide team's sums
