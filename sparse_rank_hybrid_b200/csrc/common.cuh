@@ -273,10 +273,10 @@ constexpr int kMaxWorkers = 32768;  // teams of threads that share a call's rows
 constexpr int kNormNone = 0, kNormRms = 1, kNormLayer = 2;  // slra_norm
 
 // How a call's rows are shared out: `V` vectors of eight elements a thread, `team` threads a row,
-// `workers` teams in all, in blocks of `threads` threads.  A row may be cut into `parts` that different blocks
+// `workers` teams in all, in blocks of `threads` threads, worker w on rows [w share, (w + 1) share).  A row may be cut into `parts` that different blocks
 // take (`blocks` = parts times those that hold the workers).
 struct RowPlan {
-    int V, team, threads, blocks, workers, parts;
+    int V, team, threads, blocks, workers, share, parts;
 };
 
 struct RowTensor {  // [B][L][C], C contiguous; element strides of batch and token
@@ -301,7 +301,7 @@ struct ResidualNormArgs {
     int stream_dtype, block_dtype, mod_dtype, w_dtype;
     int norm, post;
     float eps, post_eps, rs;
-    int team, workers, stages, wsum_shared;  // set by the launcher
+    int team, workers, share, stages, wsum_shared;  // set by the launcher
 };
 RowPlan residual_norm_plan(long long rows, int channels, bool backward);
 cudaError_t launch_residual_norm(const ResidualNormArgs& a, bool backward, cudaStream_t st);
@@ -337,7 +337,7 @@ struct QkRopeArgs {
     uint64_t turns[kRopeMaxPairs];  // omega / (2 pi) per pair in units of 2^-64, 0 for a pair that is not rotated
     uint8_t axis[kRopeMaxPairs];
     // set by the launcher
-    int group, team, workers, stages, parts, split_sides, part_heads[2];
+    int group, team, workers, share, stages, parts, split_sides, part_heads[2];
 };
 RowPlan qk_rope_plan(long long rows, int head_dim, int q_heads, int k_heads, int norm, bool backward);
 cudaError_t launch_qk_rope(const QkRopeArgs& a, bool backward, cudaStream_t st);

@@ -79,10 +79,10 @@ __global__ void __launch_bounds__(WIDE ? rope_threads(VQ + VK, BWD) : 128)
     // cos and sin of this step's and the next one's tokens: [2][R][2][pairs] floats a team, behind the ring
     float* table = reinterpret_cast<float*>(shared + static_cast<size_t>(a.stages) * U * blockDim.x) + in_block * 4 * R * pairs;
 
-    const long long r0 = worker_lo(a.rows, a.workers, worker), r1 = worker_lo(a.rows, a.workers, worker + 1);
-    const int n = static_cast<int>(r1 - r0);
+    const long long r0 = static_cast<long long>(worker) * a.share;
+    const int n = static_cast<int>(min(static_cast<long long>(a.share), max(0ll, a.rows - r0)));
     // teams of one warp take part in each other's shuffles, so they all loop as long as the longest
-    const int longest = WIDE ? n : static_cast<int>((a.rows + a.workers - 1) / a.workers);
+    const int longest = WIDE ? n : a.share;
     const int b0 = static_cast<int>(r0 / a.tokens), l0 = static_cast<int>(r0 % a.tokens);
     const bool need_x = !BWD || a.norm != kQkNormNone;
 
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(WIDE ? rope_threads(VQ + VK, BWD) : 128)
 }
 
 // The weights' gradients: the workers' sums joined in a fixed order, 32 columns a block.
-constexpr int kFinalWarps = 32;
+constexpr int kFinalWarps = 16;
 __global__ void __launch_bounds__(32 * kFinalWarps) qk_rope_final_kernel(const float* part, int workers, int columns,
                                                                          int q_columns, float* dwq, float* dwk) {
     __shared__ float red[kFinalWarps][32];
@@ -385,7 +385,7 @@ cudaError_t launch(QkRopeArgs a, const RowPlan& p, cudaStream_t st) {
     constexpr int R = kRows<VQ + VK, BWD>;
     const size_t stage = size_t(16) * R * (VQ + VK) * (kUnits<TX> + (BWD ? kUnits<TO> : 0)) * p.threads;
     const int per_sm = blocks_per_sm(p, BWD);
-    a.stages = ring_stages(stage, per_sm, kRingBytes / per_sm, (a.rows + a.workers - 1) / a.workers, R);
+    a.stages = ring_stages(stage, per_sm, kRingBytes / per_sm, a.share, R);
     const size_t smem = a.stages * stage + size_t(p.threads / p.team) * 2 * R * a.head_dim * sizeof(float);
     const auto kernel = qk_rope_kernel<TX, TO, VQ, VK, HALVES, BWD, WIDE>;
     if (smem > 40 * 1024) {  // 48 KB without opting in, less the static part
@@ -478,6 +478,7 @@ cudaError_t launch_qk_rope(const QkRopeArgs& args, bool backward, cudaStream_t s
     a.group = group_of(a.head_dim);
     a.team = p.team;
     a.workers = p.workers;
+    a.share = p.share;
     cudaError_t e;
     if (a.x_dtype == kF32)
         e = launch_types<float, float>(a, p, plan.VQ, backward, st);

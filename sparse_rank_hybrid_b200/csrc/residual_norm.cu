@@ -64,10 +64,10 @@ struct Place {
         size = WIDE ? blockDim.x : a.team;
         t = WIDE ? threadIdx.x : threadIdx.x % a.team;
         worker = WIDE ? blockIdx.x : blockIdx.x * (blockDim.x / a.team) + threadIdx.x / a.team;
-        const long long r0 = worker_lo(a.rows, a.workers, worker), r1 = worker_lo(a.rows, a.workers, worker + 1);
-        n = static_cast<int>(r1 - r0);
+        const long long r0 = static_cast<long long>(worker) * a.share;
+        n = static_cast<int>(min(static_cast<long long>(a.share), max(0ll, a.rows - r0)));
         // teams of one warp take part in each other's shuffles, so they all loop as long as the longest
-        longest = WIDE ? n : static_cast<int>((a.rows + a.workers - 1) / a.workers);
+        longest = WIDE ? n : a.share;
         b0 = static_cast<int>(r0 / a.tokens);
         l0 = static_cast<int>(r0 % a.tokens);
     }
@@ -537,44 +537,31 @@ constexpr int kFinalWarps = 16;
 __global__ void __launch_bounds__(32 * kFinalWarps) residual_norm_final_kernel(const __grid_constant__ ResidualNormArgs a,
                                                                                int jobs, int by_boundary) {
     __shared__ float red[3][kFinalWarps][32];
-    __shared__ int w_first, w_last, w_second;
-    __shared__ long long group;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
-    const bool in = c < a.channels;
-    const bool weights = static_cast<int>(blockIdx.y) == jobs;
-    if (threadIdx.x == 0) {
-        w_first = 0, w_last = a.workers - 1, w_second = -1, group = 0;
-        if (!weights) {
-            long long g = blockIdx.y;
-            bool whole = false;
-            if (by_boundary) {  // the modulation row that worker y + 1's first row continues
-                const long long r = worker_lo(a.rows, a.workers, static_cast<int>(blockIdx.y) + 1);
-                g = r / a.per;
-                whole = g * a.per == r || r == a.rows;
-            }
-            if (!whole) {
-                w_first = worker_of(a.rows, a.workers, g * a.per);
-                w_last = worker_of(a.rows, a.workers, (g + 1) * a.per - 1);
-                // its sums are in the workers' first slots, but in the second one of a worker that came to
-                // it from another row
-                if (worker_lo(a.rows, a.workers, w_first) < g * a.per) w_second = w_first;
-                group = g;
-            }
-            if (whole || w_first == w_last) w_last = -1;  // one worker had it all
+    const int c = blockIdx.x * 32 + lane, y = a.wpart ? static_cast<int>(blockIdx.y) - 1 : blockIdx.y;
+    const bool in = c < a.channels, weights = y < 0;  // the longest job first
+    const int rows = static_cast<int>(a.rows);
+    int w0 = 0, w1 = (rows - 1) / a.share, second = -1, g = 0;
+    if (!weights) {
+        g = y;
+        if (by_boundary) {  // the modulation row that worker y + 1's first row continues
+            const long long r = (y + 1ll) * a.share;
+            g = static_cast<int>(r / a.per);
+            if (r >= rows || r == static_cast<long long>(g) * a.per) return;
         }
+        const int first = g * a.per;
+        w0 = first / a.share;
+        w1 = (first + a.per - 1) / a.share;
+        if (w0 == w1) return;  // one worker had it all
+        // its sums are in the workers' first slots, but in the second one of a worker that came to it from
+        // another row
+        if (w0 * a.share < first) second = w0;
     }
-    __syncthreads();
-    const int w0 = w_first, w1 = w_last, second = w_second;
-    const long long g = group;
-    if (w1 < 0) return;
     float sum[3] = {0.f, 0.f, 0.f};
     if (in) {
-        const bool all = weights || a.workers <= a.rows;  // else some workers had no rows and wrote nothing
         const long long row = 3ll * a.channels;
 #pragma unroll 4
         for (int w = w0 + warp; w <= w1; w += kFinalWarps) {
-            if (!all && worker_lo(a.rows, a.workers, w) == worker_lo(a.rows, a.workers, w + 1)) continue;
             const float* p = weights ? a.wpart + w * row + c : a.part + (2ll * w + (w == second ? 1 : 0)) * row + c;
 #pragma unroll
             for (int k = 0; k < 3; ++k) sum[k] += p[static_cast<long long>(k) * a.channels];
@@ -600,7 +587,7 @@ __global__ void __launch_bounds__(32 * kFinalWarps) residual_norm_final_kernel(c
         if (a.dbias) a.dbias[c] = sum[1];
         if (a.dpost) a.dpost[c] = sum[2];
     } else {
-        const long long at = g * a.channels + c;
+        const long long at = static_cast<long long>(g) * a.channels + c;
         if (a.dshift) a.dshift[at] = sum[0];
         if (a.dscale) a.dscale[at] = value(a.weight, 1.f) * sum[1] + value(a.bias, 0.f) * sum[0];
         if (a.dgate) a.dgate[at] = value(a.post_weight, 1.f) * sum[2];
@@ -630,7 +617,7 @@ cudaError_t launch_dir(ResidualNormArgs a, const RowPlan& p, bool backward, cuda
     const size_t stage = size_t(16) * V * units * p.threads, sums = size_t(3) * V * 32 * p.threads;
     const int per_sm = blocks_per_sm(p, backward);
     const size_t room = kRingBytes / per_sm;
-    a.stages = ring_stages(stage, per_sm, room, (a.rows + a.workers - 1) / a.workers, 1);
+    a.stages = ring_stages(stage, per_sm, room, a.share, 1);
     // the weights' sums take what the ring leaves
     a.wsum_shared = backward && a.wpart && a.stages * stage + sums <= room;
     const size_t smem = a.stages * stage + (a.wsum_shared ? sums : 0);
@@ -667,6 +654,7 @@ cudaError_t launch_residual_norm(const ResidualNormArgs& args, bool backward, cu
     const RowPlan p = residual_norm_plan(a.rows, a.channels, backward);
     a.team = p.team;
     a.workers = p.workers;
+    a.share = p.share;
     cudaError_t e;
     if (a.stream_dtype == kF32)
         e = a.block_dtype == kF32    ? launch_types<float, float>(a, p, backward, st)

@@ -345,12 +345,6 @@ struct RowWalk {
     __device__ __forceinline__ void wrap() { p += back; }
 };
 
-// Rows [lo, hi) of worker w among `workers` workers sharing n rows; the worker that has row r.
-__host__ __device__ inline long long worker_lo(long long n, int workers, int w) { return n * w / workers; }
-__host__ __device__ inline int worker_of(long long n, int workers, long long r) {
-    return static_cast<int>(((r + 1) * workers - 1) / n);
-}
-
 // Threads of a block for a row of `slots` vectors, with `V` vectors a thread: rows of up to 32 vectors
 // share a block of 128 threads.
 inline void row_team(int slots, int V, RowPlan* p) {
@@ -363,11 +357,13 @@ inline void row_team(int slots, int V, RowPlan* p) {
         p->team = p->threads = ((slots + V - 1) / V + 31) / 32 * 32;
     }
 }
-// One worker a team; no more blocks than `most`, nor than rows.
+// One worker a team, on consecutive rows, as many as the blocks up to `most` make necessary.
 inline void row_workers(long long rows, int most, RowPlan* p) {
     const int teams = p->threads / p->team;
-    const long long want = (rows + teams - 1) / teams, cap = kMaxWorkers / teams < most ? kMaxWorkers / teams : most;
-    p->blocks = static_cast<int>(want < cap ? want : cap);
+    const long long cap = static_cast<long long>(kMaxWorkers / teams < most ? kMaxWorkers / teams : most) * teams;
+    p->share = static_cast<int>((rows + cap - 1) / cap);
+    const long long workers = (rows + p->share - 1) / p->share;
+    p->blocks = static_cast<int>((workers + teams - 1) / teams);
     p->workers = p->blocks * teams;
     p->parts = 1;
 }
