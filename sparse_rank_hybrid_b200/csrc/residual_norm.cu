@@ -667,7 +667,8 @@ cudaError_t launch_residual_norm(const ResidualNormArgs& args, bool backward, cu
     if (e != cudaSuccess || !backward) return e;
     const long long mods = a.rows / a.per;
     const int by_boundary = mods > p.workers ? 1 : 0;
-    const int jobs = a.part ? static_cast<int>(by_boundary ? p.workers - 1 : mods) : 0;
+    const bool whole = a.share % a.per == 0 || a.share >= a.rows;  // no modulation row has more than one worker
+    const int jobs = a.part && !whole ? static_cast<int>(by_boundary ? p.workers - 1 : mods) : 0;
     const int y = jobs + (a.wpart ? 1 : 0);
     if (y == 0) return cudaSuccess;
     residual_norm_final_kernel<<<dim3((a.channels + 31) / 32, y), 32 * kFinalWarps, 0, st>>>(a, jobs, by_boundary);

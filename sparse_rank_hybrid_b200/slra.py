@@ -625,8 +625,9 @@ def _rows(c, name, t, shape, dtype, device, field):
                          f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     if not t.is_contiguous():
         st = t.stride()
-        if st[-1] != 1 and shape[-1] != 1:
-            raise ValueError(f"{name}: expected a contiguous last dimension, got strides {st}")
+        # the struct's zeros mean contiguous: an expanded dimension must not reach it
+        if (st[-1] != 1 and shape[-1] != 1) or any(s == 0 and n > 1 for s, n in zip(st, shape)):
+            raise ValueError(f"{name}: expected a contiguous last dimension and no expanded one, got strides {st}")
         # a dimension of one element gets any valid stride
         getattr(c, field)[:] = [s if n > 1 else 8 for s, n in zip(st[:-1], shape)]
     return t.data_ptr()
@@ -656,6 +657,18 @@ def _sums_workspace(call, c, workspace, device):
     if workspace.device != device or not workspace.is_contiguous() or workspace.dtype is not torch.uint8:
         raise ValueError(f"workspace: expected a contiguous uint8 tensor on {device}")
     return workspace
+
+
+def _sums_outputs(c, out, vectors, shape, device):
+    """fp32 tensors for the gradients of the vectors that are given, out of one allocation."""
+    torch = _torch()
+    given = [(i, name) for i, name, t in vectors if t is not None]
+    if not given:
+        return
+    grads = torch.empty((len(given), *shape), dtype=torch.float32, device=device).unbind(0)
+    for (i, name), g in zip(given, grads):
+        out[i] = g
+        setattr(c, name, g.data_ptr())
 
 
 class ResidualNorm(NamedTuple):
@@ -773,8 +786,6 @@ def residual_norm_bwd(prob: ResidualNorm, x, y=None, dh=None, dx_out=None, gate=
     given gets its gradient, in fp32: dgate, dscale, dshift [batch, groups, channels], dweight, dbias,
     dpost_weight [channels].  dx may be dx_out and dy may be dh.  workspace: a uint8 tensor to reuse (None:
     allocated; it comes back in the result).  Returns ResidualNormGrads, None where there is nothing."""
-    torch = _torch()
-    empty, f32 = torch.empty, torch.float32
     row, device = prob[:3], x.device
     L = lib()
     with _On(device, stream) as handle:
@@ -790,15 +801,11 @@ def residual_norm_bwd(prob: ResidualNorm, x, y=None, dh=None, dx_out=None, gate=
             pdy = _rows(c, "dy", dy, row, block, device, "dy_strides")
         elif dy is not None:
             raise ValueError("dy: there is no y")
-        mods = (prob.batch, prob.groups, prob.channels)
-        out = []
-        for name, t in (("dgate", gate), ("dscale", scale), ("dshift", shift), ("dweight", weight), ("dbias", bias),
-                        ("dpost_weight", post_weight)):
-            g = None
-            if t is not None:
-                g = empty(mods if t.dim() == 3 else mods[2:], dtype=f32, device=device)
-                setattr(c, name, g.data_ptr())
-            out.append(g)
+        out = [None] * 6
+        _sums_outputs(c, out, ((0, "dgate", gate), (1, "dscale", scale), (2, "dshift", shift)),
+                      (prob.batch, prob.groups, prob.channels), device)
+        _sums_outputs(c, out, ((3, "dweight", weight), (4, "dbias", bias), (5, "dpost_weight", post_weight)),
+                      (prob.channels,), device)
         workspace = _sums_workspace(L.slra_residual_norm_bwd_workspace_bytes, c, workspace, device)
         _check(L.slra_residual_norm_bwd(c, px, py, pdo, pdh, pdx, pdy, workspace.data_ptr(), workspace.numel(), handle),
                "slra_residual_norm_bwd")
@@ -866,7 +873,7 @@ def _qk_rope_problem(prob, q, k, wq, wk, positions):
         c.wk = _vector("wk", wk, kv_heads * D if token else D, None if wq is None else wq.dtype, device)
         c.weight_dtype = _code(wk)
     if positions is not None:
-        n, st = positions.shape[0], positions.stride()
+        n, st = positions.shape[0] if positions.dim() == 3 else 0, positions.stride()
         if positions.shape != (n, tokens, 3) or n not in (1, batch) or positions.dtype is not _torch().int32 or \
                 positions.device != device or st[2] != 1 or (tokens > 1 and st[1] != 3):
             raise ValueError(f"positions: expected int32 [1 or {batch}, {tokens}, 3] on {device}, every sample contiguous, "

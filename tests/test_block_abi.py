@@ -216,3 +216,25 @@ def test_binding_checks_its_tensors():
         slra.qk_rope_fwd(slra.QkRope(1, 4, 1, 64), x.view(1, 4, 1, 64))
     with pytest.raises(ValueError):
         slra.residual_norm_fwd(slra.ResidualNorm(1, 4, 64), x.double())
+
+
+@pytest.mark.parametrize("t,strides", [
+    ("contiguous", (0, 0)), ("wide", (4 * 72, 72)), ("one sample", (8, 72)), ("one token", (72, 8)),
+    ("expanded", None), ("expanded whole", None), ("last dimension", None), ("shape", None), ("type", None)])
+def test_binding_strides(t, strides):
+    """The binding's strides: zeros for a contiguous tensor only, never for an expanded one (the struct's
+    zeros would read it as contiguous)."""
+    import torch
+    x = {"contiguous": torch.zeros(2, 4, 64), "wide": torch.zeros(2, 4, 72)[:, :, :64],
+         "one sample": torch.zeros(1, 4, 72)[:, :, :64], "one token": torch.zeros(2, 1, 72)[:, :, :64],
+         "expanded": torch.zeros(2, 1, 64).expand(2, 4, 64), "expanded whole": torch.zeros(64).expand(2, 4, 64),
+         "last dimension": torch.zeros(2, 64, 4).transpose(1, 2), "shape": torch.zeros(2, 4, 72),
+         "type": torch.zeros(2, 4, 64, dtype=torch.float64)}[t]
+    shape = {"one sample": (1, 4, 64), "one token": (2, 1, 64)}.get(t, (2, 4, 64))
+    c = slra._ResidualNorm()
+    if strides is None:
+        with pytest.raises(ValueError):
+            slra._rows(c, "x", x, shape, torch.float32, x.device, "x_strides")
+    else:
+        assert slra._rows(c, "x", x, shape, torch.float32, x.device, "x_strides") == x.data_ptr()
+        assert tuple(c.x_strides) == strides

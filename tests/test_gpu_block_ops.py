@@ -160,7 +160,7 @@ def check_norm_backward(p, t, d, **kw):
 
 
 # rows from one to several a worker, channels within a warp, over several warps, two vectors a thread
-SIZES = [(1, 1, 8), (1, 1, 1536), (2, 3, 24), (1, 37, 256), (3, 41, 264), (2, 150, 1032), (1, 700, 1536), (1, 5, 5120),
+SIZES = [(1, 1, 8), (1, 1, 1536), (700, 1, 48), (500, 2, 1536), (2, 3, 24), (1, 37, 256), (3, 41, 264), (2, 150, 1032), (1, 700, 1536), (1, 5, 5120),
          (1, 301, 5128), (1, 9, 8192), (5, 401, 64)]
 TYPES = [(BF, BF), (FP, BF), (HF, HF), (FP, HF), (FP, FP)]
 
@@ -283,6 +283,44 @@ def test_norm_strides_broadcasts_and_in_place():
     assert all(torch.equal(getattr(ga, n), getattr(gb, n)) for n in ("dx", "dy", "dgate", "dscale", "dshift"))
 
 
+def test_offsets_past_32_bits():
+    """Rows and heads more than 2^31 elements apart: the same bits as packed ones."""
+    far = 2 ** 30 + 8
+    buf = torch.zeros(2 * far + 4096, dtype=BF, device="cuda")
+    p, t, _ = norm_inputs(1, 3, 1024, seed=30)
+    x = buf.as_strided((1, 3, 1024), (3 * far, far, 1))
+    x.copy_(t["x"])
+    ref = slra.residual_norm_fwd(p, **t)
+    got = slra.residual_norm_fwd(p, **dict(t, x=x), x_out=x)
+    assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    rp, rt, _ = rope_inputs(3, 1, 8, 0, 128, seed=31)
+    q = buf.as_strided((3, 1, 8, 128), (far, 1024, 128, 1))
+    q.copy_(rt["q"])
+    out = slra.qk_rope_fwd(rp, q, wq=rt["wq"], out_q=q)[0]
+    assert out is q and torch.equal(q, slra.qk_rope_fwd(rp, **rt)[0])
+
+
+def test_calls_on_two_streams_at_once():
+    """Calls that overlap on the GPU share nothing: each gives its own bits."""
+    cases = []
+    for seed in (0, 1):
+        p, t, d = norm_inputs(1, 3000, 640, 3, weights=FP, seed=seed)
+        rp, rt, rd = rope_inputs(1, 3000, 5, 5, 128, norm=slra.QK_NORM_TOKEN, seed=seed)
+        ref = (*slra.residual_norm_bwd(p, **t, **d)[:7], *slra.qk_rope_bwd(rp, rt["q"], rt["k"], **rd, wq=rt["wq"], wk=rt["wk"])[:4])
+        cases.append((p, t, d, rp, rt, rd, ref, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, (p, t, d, rp, rt, rd, _, s) in enumerate(cases):
+            a = slra.residual_norm_bwd(p, **t, **d, stream=s)
+            b = slra.qk_rope_bwd(rp, rt["q"], rt["k"], **rd, wq=rt["wq"], wk=rt["wk"], stream=s)
+            got[i].append((*a[:7], *b[:4]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for run in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(run, cases[i][6]))
+
+
 def test_norm_first_block_types():
     """Without y the norm's output type is free beside an fp32 stream."""
     p, t, _ = norm_inputs(1, 13, 128, stream=FP, residual=False, seed=11)
@@ -339,19 +377,23 @@ def test_norm_deterministic_streams_and_graphs():
                                              d["dh"].data_ptr(), own["dx"].data_ptr(), own["dy"].data_ptr(), None, 0,
                                              torch.cuda.current_stream().cuda_stream) == slra.OK
     assert all(torch.equal(own[n], getattr(ref, n)) for n in names)
-    # graphs
+    # graphs: with the workspace given, with one of the binding's, with one of the library's
     torch.cuda.synchronize()
     graphs = []
-    for _ in range(2):
+    for w in (ws, ws, None):
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            res = (slra.residual_norm_fwd(p, **t), slra.residual_norm_bwd(p, **t, **d, workspace=ws))
+            res = (slra.residual_norm_fwd(p, **t), slra.residual_norm_bwd(p, **t, **d, workspace=w))
+            assert slra.lib().slra_residual_norm_bwd(
+                ctypes.byref(c), t["x"].data_ptr(), t["y"].data_ptr(), d["dx_out"].data_ptr(), d["dh"].data_ptr(),
+                own["dx"].data_ptr(), own["dy"].data_ptr(), None, 0, torch.cuda.current_stream().cuda_stream) == slra.OK
         graphs.append((g, res))
     t["x"].mul_(0.5)
     d["dh"].mul_(2.0)
     for g, _ in graphs:
         g.replay()
     f, ref = slra.residual_norm_fwd(p, **t), slra.residual_norm_bwd(p, **t, **d)
+    assert all(torch.equal(own[n], getattr(ref, n)) for n in names)
     for _, (gf, gb) in graphs:
         assert torch.equal(gf[0], f[0]) and torch.equal(gf[1], f[1])
         assert all(torch.equal(getattr(gb, n), getattr(ref, n)) for n in names)
@@ -461,7 +503,9 @@ NORMS = [slra.QK_NORM_NONE, slra.QK_NORM_HEAD, slra.QK_NORM_TOKEN]
 @pytest.mark.parametrize("pairing", [slra.ROPE_INTERLEAVED, slra.ROPE_HALVES])
 @pytest.mark.parametrize("B,L,hq,hk,D", [(1, 1, 1, 0, 64), (1, 1, 12, 12, 128), (2, 17, 2, 2, 64), (3, 50, 3, 1, 8),
                                          (1, 40, 5, 2, 96), (2, 33, 14, 2, 80), (1, 30, 24, 24, 128), (1, 21, 40, 40, 128),
-                                         (1, 9, 7, 1, 256), (1, 700, 4, 4, 64), (1, 5, 64, 64, 128), (2, 2, 1, 1, 16)])
+                                         (1, 9, 7, 1, 256), (1, 700, 4, 4, 64), (1, 5, 64, 64, 128), (2, 2, 1, 1, 16),
+                                         (1, 7, 1, 20, 64), (1, 13, 2, 9, 8), (2, 3, 33, 1, 128), (1, 9, 12, 7, 128),
+                                         (300, 1, 3, 3, 64), (1, 6, 40, 21, 128)])
 def test_rope_sizes(norm, pairing, B, L, hq, hk, D):
     p, t, d = rope_inputs(B, L, hq, hk, D, norm=norm, pairing=pairing, grid=(7, 9, 13), first_token=100, seed=L + hq)
     check_rope(p, t, d)
@@ -652,6 +696,8 @@ def test_refusals_on_the_gpu():
         slra.residual_norm_fwd(slra.ResidualNorm(1, 8, 64, groups=3), t["x"], t["y"])
     with pytest.raises(ValueError):
         slra.residual_norm_fwd(p, t["x"].cpu(), t["y"])
+    with pytest.raises(ValueError):  # an expanded row tensor
+        slra.residual_norm_fwd(p, t["x"], t["y"][:, :1].expand(1, 8, 64))
     with pytest.raises(ValueError):
         slra.residual_norm_fwd(p, t["x"], t["y"], scale=t["scale"][:, :, :32])
     with pytest.raises(slra.SlraError):  # bf16 stream with fp16 blocks
