@@ -590,7 +590,7 @@ typedef enum slra_rope_pairing { SLRA_ROPE_INTERLEAVED = 0, SLRA_ROPE_HALVES = 1
 typedef enum slra_rope_schedule { SLRA_ROPE_PER_AXIS = 0, SLRA_ROPE_SHARED = 1 } slra_rope_schedule;
 
 /*
- * RMS norm of q and k and their rotation by positions along (t, h, w), both optional:
+ * RMS norm of q and k and their rotation by positions along (t, h, w), either or both:
  *   out = R(p) (x rsqrt(mean(x^2) + eps) w), pair (a, b) -> (a cos - b sin, a sin + b cos) at the angle
  *   p[axis_j] omega_j; in fp32 (angles in double), rounded once.
  * The attention entry points rotate q and k themselves: give them the norm alone (rotate = 0).  The
@@ -612,7 +612,7 @@ typedef enum slra_rope_schedule { SLRA_ROPE_PER_AXIS = 0, SLRA_ROPE_SHARED = 1 }
  *                            sum may be below c: later pairs are not rotated.
  *   theta                    rotary base, at least 1 (default, and 0: 10000).
  *   norm                     SLRA_QK_NORM_* (default NONE); eps positive (default 1e-6).
- *   rotate                   1 (default) or 0.
+ *   rotate                   1 (default), or 0 with a norm: the norm alone.
  *   pairing, schedule        SLRA_ROPE_* (default INTERLEAVED, PER_AXIS: the attention's).
  *   x_dtype                  of q, k, dq, dk: bf16 (default), f16, f32.
  *   out_dtype                of out_q, out_k, dout_q, dout_k: x_dtype or f32 (default bf16).

@@ -212,7 +212,7 @@ slra_status derive(const slra_qk_rope* p, Heads* d) {
     if (!known_dtype(p->x_dtype) || !known_dtype(p->out_dtype) || !known_dtype(p->weight_dtype) || !positive(p->eps))
         return SLRA_ERR_INVALID_ARG;
     if (!(p->theta == 0.0 || p->theta >= 1.0) || !std::isfinite(p->theta)) return SLRA_ERR_INVALID_ARG;
-    if (p->norm == SLRA_QK_NORM_NONE && (p->wq || p->wk)) return SLRA_ERR_INVALID_ARG;
+    if (p->norm == SLRA_QK_NORM_NONE && (!p->rotate || p->wq || p->wk)) return SLRA_ERR_INVALID_ARG;
     if ((p->dwq && !p->wq) || (p->dwk && !p->wk) || (p->wk && p->kv_heads == 0)) return SLRA_ERR_INVALID_ARG;
     if (p->rotate) {
         if (p->positions) {
@@ -255,7 +255,7 @@ slra_status derive(const slra_qk_rope* p, Heads* d) {
     a.side[1].heads = static_cast<int>(p->kv_heads);
     a.side[0].weight = p->wq;
     a.side[1].weight = p->wk;
-    a.rotate = p->rotate;
+    a.H = a.W = 1;  // without a rotation every angle is zero
     a.halves = p->pairing == SLRA_ROPE_HALVES;
     a.norm = p->norm;
     a.x_dtype = p->x_dtype;

@@ -276,6 +276,7 @@ constexpr int kNormNone = 0, kNormRms = 1, kNormLayer = 2;  // slra_norm
 // `workers` teams in all, in blocks of `threads` threads, worker w on rows [w share, (w + 1) share).  A row may be cut into `parts` that different blocks
 // take (`blocks` = parts times those that hold the workers).
 struct RowPlan {
+    int VQ;  // of the V vectors those that are q's (qk_rope)
     int V, team, threads, blocks, workers, share, parts;
 };
 
@@ -329,7 +330,7 @@ struct QkRopeArgs {
     int tokens, head_dim;
     int H, W;                  // grid
     long long offset[3];
-    int rotate, halves, norm;
+    int halves, norm;
     int x_dtype, out_dtype, w_dtype;
     float eps;
     float* part;  // the weights' sums (null: none is wanted): norm over a token's heads [workers][heads * D of

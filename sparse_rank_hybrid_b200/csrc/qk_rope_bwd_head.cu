@@ -1,0 +1,10 @@
+// The backward kernels of qk_rope.cuh with a norm per head.
+#include "qk_rope.cuh"
+
+namespace slra {
+
+cudaError_t launch_qk_rope_bwd_head(const QkRopeArgs& a, const RowPlan& p, cudaStream_t st) {
+    return rope_launch_all<true, kQkNormHead>(a, p, st);
+}
+
+}  // namespace slra

@@ -146,7 +146,8 @@ HEAD, TOKEN = slra.QK_NORM_HEAD, slra.QK_NORM_TOKEN
     (dict(first_token=1, T=2), slra.ERR_NO_DEVICE), (dict(first_token=-1, T=2), slra.ERR_INVALID_ARG),
     (dict(W=1, positions=at(8)), slra.ERR_NO_DEVICE), (dict(positions=at(8) + 2), slra.ERR_ALIGNMENT),
     (dict(positions=at(8), positions_stride=71), slra.ERR_INVALID_ARG),
-    (dict(positions=at(8), positions_stride=72), slra.ERR_NO_DEVICE), (dict(W=0, rotate=0), slra.ERR_NO_DEVICE),
+    (dict(positions=at(8), positions_stride=72), slra.ERR_NO_DEVICE), (dict(W=0, rotate=0, norm=HEAD), slra.ERR_NO_DEVICE),
+    (dict(rotate=0), slra.ERR_INVALID_ARG),
     (dict(pos_offset=(0, (1 << 31) + 1, 0)), slra.ERR_INVALID_ARG), (dict(theta=float("nan")), slra.ERR_INVALID_ARG),
     (dict(theta=-1.0), slra.ERR_INVALID_ARG), (dict(theta=0.5), slra.ERR_INVALID_ARG),
     (dict(T=1 << 16, H=1 << 8, W=1 << 7), slra.ERR_INVALID_ARG), (dict(theta=1.0), slra.ERR_NO_DEVICE),
