@@ -57,9 +57,10 @@ __device__ __forceinline__ void rotate(Vec& v, const float2 (&c)[2], const float
     }
 }
 
-// A head's eight elements are consecutive (interleaved pairs) or four of each half (SPLIT).  Of a thread's
+// A vector is eight consecutive elements of a head, or four of each half (SPLIT): where the halves are paired,
+// and for fp32, where a warp's accesses then cover consecutive memory.  Of a thread's
 // vectors VQ are of q and VK of k; without the latter they are of the side that the block takes.
-template <typename TX, typename TO, int VQ, int VK, bool SPLIT, bool BWD, bool WIDE, int NORM>
+template <typename TX, typename TO, int VQ, int VK, bool HALVES, bool BWD, bool WIDE, int NORM>
 __global__ void __launch_bounds__(WIDE ? rope_threads(VQ + VK, BWD) : 128)
     qk_rope_kernel(const __grid_constant__ QkRopeArgs a) {
     // The backward is compiled for each norm: it issues so many instructions that the choice at run time
@@ -68,6 +69,7 @@ __global__ void __launch_bounds__(WIDE ? rope_threads(VQ + VK, BWD) : 128)
     constexpr int V = VQ + VK, R = kRows<V, BWD>;
     constexpr int UX = kUnits<TX>, UD = BWD ? kUnits<TO> : 0, ONE = UX + UD, U = R * V * ONE;
     using TW = typename std::conditional<BWD, TX, TO>::type;  // type of what is written
+    constexpr bool SPLIT = HALVES || sizeof(TX) == 4 || sizeof(TO) == 4;
     extern __shared__ uint4 shared[];
     __shared__ __align__(16) float scratch[kTeamScratch];
     __shared__ unsigned long long turns[kRopeMaxPairs];
@@ -186,10 +188,16 @@ __global__ void __launch_bounds__(WIDE ? rope_threads(VQ + VK, BWD) : 128)
         float2 c[R][2], sn[R][2];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const float4* cs = reinterpret_cast<const float4*>(table + (which * R + r) * 2 * pairs);
-            const float4 u = cs[place], z = cs[pairs / 4 + place];
-            c[r][0] = make_float2(u.x, u.y), c[r][1] = make_float2(u.z, u.w);
-            sn[r][0] = make_float2(z.x, z.y), sn[r][1] = make_float2(z.z, z.w);
+            const float* cs = table + (which * R + r) * 2 * pairs;
+            if constexpr (SPLIT && !HALVES) {  // two pairs of each half
+                const float2* t2 = reinterpret_cast<const float2*>(cs);
+                c[r][0] = t2[place], c[r][1] = t2[pairs / 4 + place];
+                sn[r][0] = t2[pairs / 2 + place], sn[r][1] = t2[pairs / 2 + pairs / 4 + place];
+            } else {
+                const float4 u = reinterpret_cast<const float4*>(cs)[place], z = reinterpret_cast<const float4*>(cs + pairs)[place];
+                c[r][0] = make_float2(u.x, u.y), c[r][1] = make_float2(u.z, u.w);
+                sn[r][0] = make_float2(z.x, z.y), sn[r][1] = make_float2(z.z, z.w);
+            }
         }
         which ^= 1;
         if (i + R < n) fill(which, n - i - R);
@@ -205,7 +213,7 @@ __global__ void __launch_bounds__(WIDE ? rope_threads(VQ + VK, BWD) : 128)
                 if (need_x) x[r][v] = ring.read<TX>((r * V + v) * ONE);
                 if (BWD) {
                     g[r][v] = ring.read<TO>((r * V + v) * ONE + UX);
-                    rotate<SPLIT>(g[r][v], c[r], sn[r]);
+                    rotate<HALVES>(g[r][v], c[r], sn[r]);
                 }
             }
         ring.done();
@@ -279,7 +287,7 @@ __global__ void __launch_bounds__(WIDE ? rope_threads(VQ + VK, BWD) : 128)
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 x[r][v].f[e] = mul2(x[r][v].f[e], mul2(w[v].f[e], both(rd[r][v])));
-                        rotate<SPLIT>(x[r][v], c[r], sn[r]);
+                        rotate<HALVES>(x[r][v], c[r], sn[r]);
                         if (on[v]) store_vec<TW, SPLIT>(out, x[r][v], gap);
                     } else {
                         if (norm) {
