@@ -13,7 +13,7 @@ __global__ void __launch_bounds__(32 * kFinalWarps) qk_rope_final_kernel(const f
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float sum = 0.f;
     if (c < columns)
-#pragma unroll 4
+#pragma unroll 8
         for (int w = warp; w < workers; w += kFinalWarps) sum += part[static_cast<long long>(w) * columns + c];
     red[warp][lane] = sum;
     __syncthreads();

@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(32 * kFinalWarps) residual_norm_final_kernel(c
     float sum[3] = {0.f, 0.f, 0.f};
     if (in) {
         const long long row = 3ll * a.channels;
-#pragma unroll 4
+#pragma unroll 8
         for (int w = w0 + warp; w <= w1; w += kFinalWarps) {
             const float* p = weights ? a.wpart + w * row + c : a.part + (2ll * w + (w == second ? 1 : 0)) * row + c;
 #pragma unroll

@@ -634,11 +634,15 @@ def _rows(c, name, t, shape, dtype, device, field):
 
 
 def _like(t, shape, dtype):
-    """A new contiguous tensor of this shape on t's device (the quicker of torch's ways where t is one)."""
+    """A new contiguous tensor of this shape on t's device, by the quickest of torch's ways."""
     torch = _torch()
     if t.is_contiguous():
         return torch.empty_like(t) if t.dtype is dtype else torch.empty_like(t, dtype=dtype)
-    return torch.empty(shape, dtype=dtype, device=t.device)
+    strides, n = [], 1
+    for k in reversed(shape):
+        strides.append(n)
+        n *= k
+    return torch.empty_strided(shape, strides[::-1], dtype=dtype, device=t.device)
 
 
 def _vector(name, t, n, dtype, device):
@@ -653,22 +657,10 @@ def _sums_workspace(call, c, workspace, device):
     one: the call itself then says why)."""
     torch = _torch()
     if workspace is None:
-        return torch.empty(max(call(c), 256), dtype=torch.uint8, device=device)
+        return torch.empty_strided((max(call(c), 256),), (1,), dtype=torch.uint8, device=device)
     if workspace.device != device or not workspace.is_contiguous() or workspace.dtype is not torch.uint8:
         raise ValueError(f"workspace: expected a contiguous uint8 tensor on {device}")
     return workspace
-
-
-def _sums_outputs(c, out, vectors, shape, device):
-    """fp32 tensors for the gradients of the vectors that are given, out of one allocation."""
-    torch = _torch()
-    given = [(i, name) for i, name, t in vectors if t is not None]
-    if not given:
-        return
-    grads = torch.empty((len(given), *shape), dtype=torch.float32, device=device).unbind(0)
-    for (i, name), g in zip(given, grads):
-        out[i] = g
-        setattr(c, name, g.data_ptr())
 
 
 class ResidualNorm(NamedTuple):
@@ -801,11 +793,14 @@ def residual_norm_bwd(prob: ResidualNorm, x, y=None, dh=None, dx_out=None, gate=
             pdy = _rows(c, "dy", dy, row, block, device, "dy_strides")
         elif dy is not None:
             raise ValueError("dy: there is no y")
-        out = [None] * 6
-        _sums_outputs(c, out, ((0, "dgate", gate), (1, "dscale", scale), (2, "dshift", shift)),
-                      (prob.batch, prob.groups, prob.channels), device)
-        _sums_outputs(c, out, ((3, "dweight", weight), (4, "dbias", bias), (5, "dpost_weight", post_weight)),
-                      (prob.channels,), device)
+        f32, mods, out = _torch().float32, (prob.batch, prob.groups, prob.channels), []
+        for name, t in (("dgate", gate), ("dscale", scale), ("dshift", shift), ("dweight", weight), ("dbias", bias),
+                        ("dpost_weight", post_weight)):
+            g = None
+            if t is not None:
+                g = _like(t, mods if t.dim() == 3 else mods[2:], f32)
+                setattr(c, name, g.data_ptr())
+            out.append(g)
         workspace = _sums_workspace(L.slra_residual_norm_bwd_workspace_bytes, c, workspace, device)
         _check(L.slra_residual_norm_bwd(c, px, py, pdo, pdh, pdx, pdy, workspace.data_ptr(), workspace.numel(), handle),
                "slra_residual_norm_bwd")
@@ -915,9 +910,7 @@ def qk_rope_bwd(prob: QkRope, q, k, dout_q, dout_k=None, wq=None, wk=None, posit
     weights' in fp32 where they are given.  dout_q, dout_k: q's type or fp32, any strides.  dq, dk may be
     given (e.g. views of one fused gradient, or dout_q, dout_k themselves where the types agree).
     workspace: as for residual_norm_bwd.  Returns QkRopeGrads, None where there is nothing."""
-    torch = _torch()
-    empty, f32 = torch.empty, torch.float32
-    device = q.device
+    f32, device = _torch().float32, q.device
     L = lib()
     if (dout_k is not None) != (prob.kv_heads > 0):
         raise ValueError(f"dout_k: the problem has {prob.kv_heads} key heads")
@@ -938,10 +931,10 @@ def qk_rope_bwd(prob: QkRope, q, k, dout_q, dout_k=None, wq=None, wk=None, posit
         elif dk is not None:
             raise ValueError("dk: there is no k")
         if wq is not None:
-            dwq = empty(wq.shape, dtype=f32, device=device)
+            dwq = _like(wq, wq.shape, f32)
             c.dwq = dwq.data_ptr()
         if wk is not None:
-            dwk = empty(wk.shape, dtype=f32, device=device)
+            dwk = _like(wk, wk.shape, f32)
             c.dwk = dwk.data_ptr()
         workspace = _sums_workspace(L.slra_qk_rope_bwd_workspace_bytes, c, workspace, device)
         _check(L.slra_qk_rope_bwd(c, pq, pk, pgq, pgk, pdq, pdk, workspace.data_ptr(), workspace.numel(), handle),
