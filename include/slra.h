@@ -32,6 +32,12 @@
  *                 sqrt(mean(O_lowrank,i^2) + 1e-6), g_i = sigmoid(q_i . Wg + bg) on the raw query; the
  *                 pages print no formula, this is the library's reading of their description)
  *
+ * Around the attention in a transformer block, forward and backward (the last part of this file):
+ *   slra_residual_norm   gated residual, optionally with a norm of the block's output, and the modulated
+ *                        norm that the next block starts with, in one pass;
+ *   slra_qk_rope         QK norm (per head or over a token's heads) and the rotation along (t, h, w), for
+ *                        grids, listed positions and single tokens.
+ *
  * Conventions for every entry point:
  *   - Device pointers unless stated otherwise.  The caller owns every buffer; nothing the caller
  *     passes is retained after a call returns (the library itself keeps, per device, the two copy
