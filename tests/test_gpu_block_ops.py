@@ -181,6 +181,31 @@ def test_norm_types(stream, block, C):
         check_norm_backward(p, t, d)
 
 
+@pytest.mark.parametrize("stream,block", TYPES)
+def test_norm_widest_rows(stream, block):
+    """8192 channels: one step of the ring for fp32, the weights' sums outside shared memory."""
+    p, t, d = norm_inputs(1, 300, 8192, 2, stream, block, weights=FP, post=slra.NORM_RMS, seed=40)
+    check_norm_forward(p, t)
+    check_norm_backward(p, t, d)
+
+
+@pytest.mark.parametrize("mod", [BF, HF, FP])
+@pytest.mark.parametrize("weights", [BF, HF, FP])
+@pytest.mark.parametrize("stream", [FP, BF])
+def test_norm_vector_types(mod, weights, stream):
+    """Modulation and weights of any type, whatever the rows'."""
+    p, t, d = norm_inputs(2, 14, 152, 2, stream, BF, mod, weights=weights, post=slra.NORM_RMS, seed=41)
+    check_norm_forward(p, t)
+    check_norm_backward(p, t, d)
+
+
+@pytest.mark.parametrize("rs", [0.0, -2.0, 1e-3])
+def test_norm_residual_scale(rs):
+    p, t, d = norm_inputs(1, 40, 512, rs=rs, seed=42)
+    check_norm_forward(p, t)
+    check_norm_backward(p, t, d)
+
+
 @pytest.mark.parametrize("norm", [slra.NORM_NONE, slra.NORM_RMS, slra.NORM_LAYER])
 @pytest.mark.parametrize("post", [slra.NORM_NONE, slra.NORM_RMS])
 @pytest.mark.parametrize("weights", [None, FP])
@@ -505,7 +530,7 @@ NORMS = [slra.QK_NORM_NONE, slra.QK_NORM_HEAD, slra.QK_NORM_TOKEN]
                                          (1, 40, 5, 2, 96), (2, 33, 14, 2, 80), (1, 30, 24, 24, 128), (1, 21, 40, 40, 128),
                                          (1, 9, 7, 1, 256), (1, 700, 4, 4, 64), (1, 5, 64, 64, 128), (2, 2, 1, 1, 16),
                                          (1, 7, 1, 20, 64), (1, 13, 2, 9, 8), (2, 3, 33, 1, 128), (1, 9, 12, 7, 128),
-                                         (300, 1, 3, 3, 64), (1, 6, 40, 21, 128)])
+                                         (300, 1, 3, 3, 64), (1, 6, 40, 21, 128), (1, 3, 1000, 700, 8)])
 def test_rope_sizes(norm, pairing, B, L, hq, hk, D):
     p, t, d = rope_inputs(B, L, hq, hk, D, norm=norm, pairing=pairing, grid=(7, 9, 13), first_token=100, seed=L + hq)
     check_rope(p, t, d)
@@ -546,6 +571,18 @@ def test_rope_listed_positions(shared, hq):
     listed = torch.stack([n // 30, n // 6 % 5, n % 6], 1)[None].int().contiguous()
     a, b = slra.qk_rope_fwd(grid, **t), slra.qk_rope_fwd(p, **t, positions=listed)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_rope_position_slices_and_single_weights():
+    """Positions as a slice of a longer list; a weight for one side only; weights of another type."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    pos = torch.randint(0, 900, (3, 60, 3), generator=g, device="cuda", dtype=torch.int32)[:, 11:11 + 20]
+    for side in ("wq", "wk"):
+        for weights in (BF, HF, FP):
+            for norm in (slra.QK_NORM_HEAD, slra.QK_NORM_TOKEN):
+                p, t, d = rope_inputs(3, 20, 6, 4, 64, BF, weights=weights, norm=norm, seed=8)
+                t[side] = None
+                check_rope(p, t, d, pos)
 
 
 def test_rope_far_positions():
