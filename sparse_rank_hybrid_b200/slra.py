@@ -581,40 +581,27 @@ def _code(t) -> int:
 
 @functools.lru_cache(maxsize=None)
 def _current_stream():
-    """device -> handle of its current stream; the direct query where this torch has one (a fraction of the
-    time that making a Stream object takes)."""
+    """device index -> handle of its current stream; the direct query where this torch has one (a fraction of
+    the time that making a Stream object takes)."""
     torch = _torch()
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is not None:
-        return lambda device: raw(device.index)
-    return lambda device: torch.cuda.current_stream(device).cuda_stream
+    return raw if raw is not None else lambda index: torch.cuda.current_stream(index).cuda_stream
 
 
-class _On:
-    """The tensors' device made current, and `stream` (None: that device's current stream) with it; what is
-    allocated inside belongs to that stream.  Gives the stream's handle."""
-    __slots__ = ("ctx", "device")
-
-    def __init__(self, device, stream):
-        torch = _torch()
-        if device.type != "cuda":
-            raise ValueError(f"expected CUDA tensors, got {device}")
-        self.ctx, self.device = None, device
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
-            self.ctx = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != device.index:
-            self.ctx = torch.cuda.stream(torch.cuda.current_stream(device))
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return _current_stream()(self.device)
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _elsewhere(t, stream):
+    """None where t's device is current and `stream` is None; else what makes the device current and the
+    stream (None: the device's current one) with it, so that what is allocated inside belongs to it."""
+    device = t.device
+    if device.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got {device}")
+    torch = _torch()
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return None
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+    return torch.cuda.stream(stream)
 
 
 def _rows(c, name, t, shape, dtype, device, field):
@@ -715,24 +702,25 @@ def _residual_norm_problem(prob, x, y, h, gate, scale, shift, weight, bias, post
     mods, dtype = (batch, groups, channels), None
     for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
         if t is not None:
-            if t.shape != mods or (dtype is not None and t.dtype is not dtype) or t.device != device or \
-                    (channels > 1 and t.stride(2) != 1):
-                raise ValueError(f"{name}: expected {mods} on {device} with a contiguous last dimension, of one type with "
-                                 f"the other modulation vectors, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on "
-                                 f"{t.device}")
             if dtype is None:
                 dtype = t.dtype
                 c.mod_dtype = _code(t)
+            st = None if t.is_contiguous() else t.stride()
+            if t.shape != mods or t.dtype is not dtype or t.device != device or (st and channels > 1 and st[2] != 1):
+                raise ValueError(f"{name}: expected {mods} on {device} with a contiguous last dimension, of one type with "
+                                 f"the other modulation vectors, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on "
+                                 f"{t.device}")
             setattr(c, name, t.data_ptr())
-            if not t.is_contiguous():
-                getattr(c, name + "_strides")[:] = (t.stride(0) if batch > 1 else 0, t.stride(1) if groups > 1 else 0)
-    dtype = None
-    for name, t in (("weight", weight), ("bias", bias), ("post_weight", post_weight)):
-        if t is not None:
-            setattr(c, name, _vector(name, t, channels, dtype, device))
-            if dtype is None:
-                dtype = t.dtype
-                c.weight_dtype = _code(t)
+            if st:
+                getattr(c, name + "_strides")[:] = (st[0] if batch > 1 else 0, st[1] if groups > 1 else 0)
+    if weight is not None or bias is not None or post_weight is not None:
+        dtype = None
+        for name, t in (("weight", weight), ("bias", bias), ("post_weight", post_weight)):
+            if t is not None:
+                setattr(c, name, _vector(name, t, channels, dtype, device))
+                if dtype is None:
+                    dtype = t.dtype
+                    c.weight_dtype = _code(t)
     return c, block.dtype, px, py
 
 
@@ -745,29 +733,33 @@ def residual_norm_fwd(prob: ResidualNorm, x, y=None, gate=None, scale=None, shif
     torch dtype; for a call without y, default x's).  Rows may be strided, x_out may be x and h may be y.
     Returns (x_out, h): x itself where there is no y, None for h with NORM_NONE."""
     row, device = prob[:3], x.device
-    with _On(device, stream) as handle:
-        c, block, px, py = _residual_norm_problem(prob, x, y, h, gate, scale, shift, weight, bias, post_weight)
-        if h_dtype is not None and y is None and h is None:
-            block = h_dtype
-            c.block_dtype = _codes()[h_dtype]
-        po = ph = None
-        if y is None:
-            if x_out is not None:
-                raise ValueError("x_out: there is no y to add")
-        elif x_out is None:
-            x_out = _like(x, row, x.dtype)
-            po = x_out.data_ptr()
-        else:
-            po = _rows(c, "x_out", x_out, row, x.dtype, device, "x_out_strides")
-        if prob.norm == NORM_NONE:
-            if h is not None:
-                raise ValueError("h: the problem has no norm")
-        elif h is None:
-            h = _like(x if y is None else y, row, block)
-            ph = h.data_ptr()
-        else:
-            ph = _rows(c, "h", h, row, block, device, "h_strides")
-        _check(lib().slra_residual_norm_fwd(c, px, py, po, ph, handle), "slra_residual_norm_fwd")
+    other = _elsewhere(x, stream)
+    if other is not None:
+        with other:
+            return residual_norm_fwd(prob, x, y, gate, scale, shift, weight, bias, post_weight, x_out, h, h_dtype)
+    handle = _current_stream()(x.device.index)
+    c, block, px, py = _residual_norm_problem(prob, x, y, h, gate, scale, shift, weight, bias, post_weight)
+    if h_dtype is not None and y is None and h is None:
+        block = h_dtype
+        c.block_dtype = _codes()[h_dtype]
+    po = ph = None
+    if y is None:
+        if x_out is not None:
+            raise ValueError("x_out: there is no y to add")
+    elif x_out is None:
+        x_out = _like(x, row, x.dtype)
+        po = x_out.data_ptr()
+    else:
+        po = _rows(c, "x_out", x_out, row, x.dtype, device, "x_out_strides")
+    if prob.norm == NORM_NONE:
+        if h is not None:
+            raise ValueError("h: the problem has no norm")
+    elif h is None:
+        h = _like(x if y is None else y, row, block)
+        ph = h.data_ptr()
+    else:
+        ph = _rows(c, "h", h, row, block, device, "h_strides")
+    _check(lib().slra_residual_norm_fwd(c, px, py, po, ph, handle), "slra_residual_norm_fwd")
     return (x if y is None else x_out), h
 
 
@@ -780,30 +772,34 @@ def residual_norm_bwd(prob: ResidualNorm, x, y=None, dh=None, dx_out=None, gate=
     allocated; it comes back in the result).  Returns ResidualNormGrads, None where there is nothing."""
     row, device = prob[:3], x.device
     L = lib()
-    with _On(device, stream) as handle:
-        c, block, px, py = _residual_norm_problem(prob, x, y, dh, gate, scale, shift, weight, bias, post_weight)
-        pdh = None if dh is None else _rows(c, "dh", dh, row, block, device, "h_strides")
-        pdo = None if dx_out is None else _rows(c, "dx_out", dx_out, row, x.dtype, device, "x_out_strides")
-        if dx is None:
-            dx = _like(x, row, x.dtype)
-        pdx, pdy = _rows(c, "dx", dx, row, x.dtype, device, "dx_strides"), None
-        if y is not None:
-            if dy is None:
-                dy = _like(y, row, block)
-            pdy = _rows(c, "dy", dy, row, block, device, "dy_strides")
-        elif dy is not None:
-            raise ValueError("dy: there is no y")
-        f32, mods, out = _torch().float32, (prob.batch, prob.groups, prob.channels), []
-        for name, t in (("dgate", gate), ("dscale", scale), ("dshift", shift), ("dweight", weight), ("dbias", bias),
-                        ("dpost_weight", post_weight)):
-            g = None
-            if t is not None:
-                g = _like(t, mods if t.dim() == 3 else mods[2:], f32)
-                setattr(c, name, g.data_ptr())
-            out.append(g)
-        workspace = _sums_workspace(L.slra_residual_norm_bwd_workspace_bytes, c, workspace, device)
-        _check(L.slra_residual_norm_bwd(c, px, py, pdo, pdh, pdx, pdy, workspace.data_ptr(), workspace.numel(), handle),
-               "slra_residual_norm_bwd")
+    other = _elsewhere(x, stream)
+    if other is not None:
+        with other:
+            return residual_norm_bwd(prob, x, y, dh, dx_out, gate, scale, shift, weight, bias, post_weight, dx, dy, workspace)
+    handle = _current_stream()(x.device.index)
+    c, block, px, py = _residual_norm_problem(prob, x, y, dh, gate, scale, shift, weight, bias, post_weight)
+    pdh = None if dh is None else _rows(c, "dh", dh, row, block, device, "h_strides")
+    pdo = None if dx_out is None else _rows(c, "dx_out", dx_out, row, x.dtype, device, "x_out_strides")
+    if dx is None:
+        dx = _like(x, row, x.dtype)
+    pdx, pdy = _rows(c, "dx", dx, row, x.dtype, device, "dx_strides"), None
+    if y is not None:
+        if dy is None:
+            dy = _like(y, row, block)
+        pdy = _rows(c, "dy", dy, row, block, device, "dy_strides")
+    elif dy is not None:
+        raise ValueError("dy: there is no y")
+    f32, mods, out = _torch().float32, (prob.batch, prob.groups, prob.channels), []
+    for name, t in (("dgate", gate), ("dscale", scale), ("dshift", shift), ("dweight", weight), ("dbias", bias),
+                    ("dpost_weight", post_weight)):
+        g = None
+        if t is not None:
+            g = _like(t, mods if t.dim() == 3 else mods[2:], f32)
+            setattr(c, name, g.data_ptr())
+        out.append(g)
+    workspace = _sums_workspace(L.slra_residual_norm_bwd_workspace_bytes, c, workspace, device)
+    _check(L.slra_residual_norm_bwd(c, px, py, pdo, pdh, pdx, pdy, workspace.data_ptr(), workspace.numel(), handle),
+           "slra_residual_norm_bwd")
     return ResidualNormGrads(dx, dy, *out, workspace)
 
 
@@ -884,23 +880,27 @@ def qk_rope_fwd(prob: QkRope, q, k=None, wq=None, wk=None, positions=None, out_q
     [heads * head_dim] with QK_NORM_TOKEN); positions: int32 [1 or batch, tokens, 3] in place of the grid.
     out_q may be q and out_k may be k.  Returns (out_q, out_k); out_k is None without k."""
     device = q.device
-    with _On(device, stream) as handle:
-        c, pq, pk = _qk_rope_problem(prob, q, k, wq, wk, positions)
-        code = prob.out_dtype
-        dtype = q.dtype if code is None else _types()[code]
-        c.out_dtype = c.x_dtype if code is None else code
-        shape, po_k = (prob.batch, prob.tokens, prob.heads, prob.head_dim), None
-        if out_q is None:
-            out_q = _like(q, shape, dtype)
-        po_q = _rows(c, "out_q", out_q, shape, dtype, device, "out_q_strides")
-        if k is not None:
-            shape = (prob.batch, prob.tokens, prob.kv_heads, prob.head_dim)
-            if out_k is None:
-                out_k = _like(k, shape, dtype)
-            po_k = _rows(c, "out_k", out_k, shape, dtype, device, "out_k_strides")
-        elif out_k is not None:
-            raise ValueError("out_k: there is no k")
-        _check(lib().slra_qk_rope_fwd(c, pq, pk, po_q, po_k, handle), "slra_qk_rope_fwd")
+    other = _elsewhere(q, stream)
+    if other is not None:
+        with other:
+            return qk_rope_fwd(prob, q, k, wq, wk, positions, out_q, out_k)
+    handle = _current_stream()(q.device.index)
+    c, pq, pk = _qk_rope_problem(prob, q, k, wq, wk, positions)
+    code = prob.out_dtype
+    dtype = q.dtype if code is None else _types()[code]
+    c.out_dtype = c.x_dtype if code is None else code
+    shape, po_k = (prob.batch, prob.tokens, prob.heads, prob.head_dim), None
+    if out_q is None:
+        out_q = _like(q, shape, dtype)
+    po_q = _rows(c, "out_q", out_q, shape, dtype, device, "out_q_strides")
+    if k is not None:
+        shape = (prob.batch, prob.tokens, prob.kv_heads, prob.head_dim)
+        if out_k is None:
+            out_k = _like(k, shape, dtype)
+        po_k = _rows(c, "out_k", out_k, shape, dtype, device, "out_k_strides")
+    elif out_k is not None:
+        raise ValueError("out_k: there is no k")
+    _check(lib().slra_qk_rope_fwd(c, pq, pk, po_q, po_k, handle), "slra_qk_rope_fwd")
     return out_q, out_k
 
 
@@ -914,29 +914,33 @@ def qk_rope_bwd(prob: QkRope, q, k, dout_q, dout_k=None, wq=None, wk=None, posit
     L = lib()
     if (dout_k is not None) != (prob.kv_heads > 0):
         raise ValueError(f"dout_k: the problem has {prob.kv_heads} key heads")
-    with _On(device, stream) as handle:
-        c, pq, pk = _qk_rope_problem(prob, q, k, wq, wk, positions)
-        c.out_dtype = _code(dout_q)
-        shape, dwq, dwk, pgk, pdk = (prob.batch, prob.tokens, prob.heads, prob.head_dim), None, None, None, None
-        pgq = _rows(c, "dout_q", dout_q, shape, None, device, "out_q_strides")
-        if dq is None:
-            dq = _like(q, shape, q.dtype)
-        pdq = _rows(c, "dq", dq, shape, q.dtype, device, "dq_strides")
-        if k is not None:
-            shape = (prob.batch, prob.tokens, prob.kv_heads, prob.head_dim)
-            pgk = _rows(c, "dout_k", dout_k, shape, dout_q.dtype, device, "out_k_strides")
-            if dk is None:
-                dk = _like(k, shape, k.dtype)
-            pdk = _rows(c, "dk", dk, shape, q.dtype, device, "dk_strides")
-        elif dk is not None:
-            raise ValueError("dk: there is no k")
-        if wq is not None:
-            dwq = _like(wq, wq.shape, f32)
-            c.dwq = dwq.data_ptr()
-        if wk is not None:
-            dwk = _like(wk, wk.shape, f32)
-            c.dwk = dwk.data_ptr()
-        workspace = _sums_workspace(L.slra_qk_rope_bwd_workspace_bytes, c, workspace, device)
-        _check(L.slra_qk_rope_bwd(c, pq, pk, pgq, pgk, pdq, pdk, workspace.data_ptr(), workspace.numel(), handle),
-               "slra_qk_rope_bwd")
+    other = _elsewhere(q, stream)
+    if other is not None:
+        with other:
+            return qk_rope_bwd(prob, q, k, dout_q, dout_k, wq, wk, positions, dq, dk, workspace)
+    handle = _current_stream()(q.device.index)
+    c, pq, pk = _qk_rope_problem(prob, q, k, wq, wk, positions)
+    c.out_dtype = _code(dout_q)
+    shape, dwq, dwk, pgk, pdk = (prob.batch, prob.tokens, prob.heads, prob.head_dim), None, None, None, None
+    pgq = _rows(c, "dout_q", dout_q, shape, None, device, "out_q_strides")
+    if dq is None:
+        dq = _like(q, shape, q.dtype)
+    pdq = _rows(c, "dq", dq, shape, q.dtype, device, "dq_strides")
+    if k is not None:
+        shape = (prob.batch, prob.tokens, prob.kv_heads, prob.head_dim)
+        pgk = _rows(c, "dout_k", dout_k, shape, dout_q.dtype, device, "out_k_strides")
+        if dk is None:
+            dk = _like(k, shape, k.dtype)
+        pdk = _rows(c, "dk", dk, shape, q.dtype, device, "dk_strides")
+    elif dk is not None:
+        raise ValueError("dk: there is no k")
+    if wq is not None:
+        dwq = _like(wq, wq.shape, f32)
+        c.dwq = dwq.data_ptr()
+    if wk is not None:
+        dwk = _like(wk, wk.shape, f32)
+        c.dwk = dwk.data_ptr()
+    workspace = _sums_workspace(L.slra_qk_rope_bwd_workspace_bytes, c, workspace, device)
+    _check(L.slra_qk_rope_bwd(c, pq, pk, pgq, pgk, pdq, pdk, workspace.data_ptr(), workspace.numel(), handle),
+           "slra_qk_rope_bwd")
     return QkRopeGrads(dq, dk, dwq, dwk, workspace)
