@@ -302,7 +302,8 @@ struct ResidualNormArgs {
     int stream_dtype, block_dtype, mod_dtype, w_dtype;
     int norm, post;
     float eps, post_eps, rs;
-    int team, workers, share, stages, wsum_shared;  // set by the launcher
+    // set by the launcher
+    int team, teams, workers, blocks, share, stages, wsum_shared, mod_units, weight_units;
 };
 RowPlan residual_norm_plan(long long rows, int channels, bool backward);
 cudaError_t launch_residual_norm(const ResidualNormArgs& a, bool backward, cudaStream_t st);

@@ -5,29 +5,36 @@
 namespace slra {
 namespace {
 
-// The weights' gradients: the workers' sums joined in a fixed order, 32 columns a block.
-constexpr int kFinalWarps = 16;
+// The weights' gradients: the workers' sums joined in a fixed order, 32 columns a cluster.
 __global__ void __launch_bounds__(32 * kFinalWarps) qk_rope_final_kernel(const float* part, int workers, int columns,
-                                                                         int q_columns, float* dwq, float* dwk) {
-    __shared__ float red[kFinalWarps][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-    float sum = 0.f;
+                                                                         int q_columns, float* dwq, float* dwk, int splits) {
+    __shared__ float red[kFinalWarps][32], total[1][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x / splits * 32 + lane;
+    float sum[1] = {0.f};
     if (c < columns)
 #pragma unroll 8
-        for (int w = warp; w < workers; w += kFinalWarps) sum += part[static_cast<long long>(w) * columns + c];
-    red[warp][lane] = sum;
+        for (int w = warp + blockIdx.x % splits * kFinalWarps; w < workers; w += kFinalWarps * splits)
+            sum[0] += part[static_cast<long long>(w) * columns + c];
+    red[warp][lane] = sum[0];
     __syncthreads();
-    if (warp != 0 || c >= columns) return;
-    sum = 0.f;
-    for (int w = 0; w < kFinalWarps; ++w) sum += red[w][lane];
+    if (warp == 0) {
+        sum[0] = 0.f;
+        for (int w = 0; w < kFinalWarps; ++w) sum[0] += red[w][lane];
+        total[0][lane] = sum[0];
+    }
+    if (splits > 1) join_cluster<1>(total, sum, splits);
+    if (warp != 0 || c >= columns || blockIdx.x % splits != 0) return;
     if (c < q_columns) {
-        if (dwq) dwq[c] = sum;
+        if (dwq) dwq[c] = sum[0];
     } else if (dwk) {
-        dwk[c - q_columns] = sum;
+        dwk[c - q_columns] = sum[0];
     }
 }
 
-int group_of(int head_dim) {
+// Threads of a head.  The norm per head sums over them by exchanges in a warp; else no more than it has vectors
+// (heads of 80 then idle no thread in three).
+int group_of(int head_dim, int norm) {
+    if (norm != kQkNormHead) return head_dim / 8;
     int g = 1;
     while (g * 8 < head_dim) g *= 2;
     return g;
@@ -45,7 +52,7 @@ struct RopePlan {
 
 RopePlan plan_of(long long rows, int head_dim, int q_heads, int k_heads, int norm, bool backward) {
     RopePlan best;
-    const int G = group_of(head_dim);
+    const int G = group_of(head_dim, norm);
     long long least = -1;
     // parts of the heads, or sides apart (parts 0); vectors a thread of q and of k, or of the side
     for (int parts = 0; parts <= 16; ++parts) {
@@ -58,7 +65,7 @@ RopePlan plan_of(long long rows, int head_dim, int q_heads, int k_heads, int nor
             row_team(std::max((hq * G + vq - 1) / vq, hk * G), 1, &p);
             p.VQ = vq;
             p.V = vq + (hk ? 1 : 0);
-            if (p.team % G != 0 || p.threads > rope_threads(p.V, backward) || (p.team <= 32 && vq > 1)) continue;
+            if ((vq > 1 && p.team % G != 0) || p.threads > rope_threads(p.V, backward) || (p.team <= 32 && vq > 1)) continue;
             // Thread-steps of a row: a step costs about as much as one vector besides its vectors, and an
             // entry of the table as much as another; registers that a thread needs are threads that the SM
             // lacks.  Sides apart cost both blocks the table, and leave threads idle where they are unequal.
@@ -98,7 +105,7 @@ cudaError_t launch_qk_rope(const QkRopeArgs& args, bool backward, cudaStream_t s
     a.split_sides = plan.split_sides;
     a.part_heads[0] = plan.part_heads[0];
     a.part_heads[1] = plan.part_heads[1];
-    a.group = group_of(a.head_dim);
+    a.group = group_of(a.head_dim, a.norm);
     a.team = p.team;
     a.workers = p.workers;
     a.share = p.share;
@@ -111,9 +118,10 @@ cudaError_t launch_qk_rope(const QkRopeArgs& args, bool backward, cudaStream_t s
     const int q_columns = a.head_dim * (each ? a.side[0].heads : 1);
     const int k_columns = a.head_dim * (each ? a.side[1].heads : a.side[1].heads > 0);
     const int columns = q_columns + k_columns;
-    qk_rope_final_kernel<<<(columns + 31) / 32, 32 * kFinalWarps, 0, st>>>(
-        a.part, each ? p.workers : p.workers * p.parts, columns, q_columns, a.side[0].dweight, a.side[1].dweight);
-    return cudaGetLastError();
+    const int workers = each ? p.workers : p.workers * p.parts;
+    const int splits = join_splits(workers, (columns + 31) / 32);
+    return launch_join(qk_rope_final_kernel, (columns + 31ll) / 32 * splits, splits, st, a.part, workers, columns, q_columns,
+                       a.side[0].dweight, a.side[1].dweight, splits);
 }
 
 cudaError_t launch_qk_rope_fwd(const QkRopeArgs& a, const RowPlan& p, cudaStream_t st) {

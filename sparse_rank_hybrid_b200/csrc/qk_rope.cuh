@@ -359,7 +359,9 @@ inline int rope_blocks_per_sm(const RowPlan& p, bool backward, bool norm) {
     const int wide[3][4] = {{0, 80, 96, 128}, {0, 96, 120, 168}, {0, 48, 64, 64}};
     const int narrow[3][3] = {{0, 80, 120}, {0, 128, 136}, {0, 64, 64}};
     const int kind = !backward ? 0 : norm ? 1 : 2;
-    return std::max(1, 65536 / ((p.team <= 32 ? narrow[kind][p.V] : wide[kind][p.V]) * p.threads));
+    // a quarter of the registers and of the warps each to an SM's four parts
+    const int warps = 4 * (16384 / (32 * (p.team <= 32 ? narrow[kind][p.V] : wide[kind][p.V])));
+    return std::max(1, warps * 32 / p.threads);
 }
 
 template <typename TX, typename TO, int VQ, int VK, bool HALVES, bool BWD, bool WIDE, int NORM>

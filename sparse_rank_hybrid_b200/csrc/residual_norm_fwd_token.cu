@@ -1,0 +1,10 @@
+// Gated residual and modulated norm: forward, a modulation row for each row (residual_norm.cuh).
+#include "residual_norm.cuh"
+
+namespace slra {
+
+cudaError_t launch_residual_norm_fwd_token(const ResidualNormArgs& a, const RowPlan& p, cudaStream_t st) {
+    return launch_rows<false, true>(a, p, st);
+}
+
+}  // namespace slra

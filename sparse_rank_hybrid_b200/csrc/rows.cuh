@@ -378,4 +378,51 @@ inline int ring_stages(size_t stage, int blocks_per_sm, size_t room, long long m
     return n;
 }
 
+// The sums of partial sums: kernels of `kFinalWarps` warps a block.  Where a job has many, the blocks of a
+// cluster share it.
+constexpr int kFinalWarps = 16;
+
+// Adds the totals of the cluster's other blocks to warp 0's `sum` in its first block, in the blocks' order.
+template <int N>
+__device__ __forceinline__ void join_cluster(float (&total)[N][32], float (&sum)[N], int splits) {
+    auto barrier = []() {
+        asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    };
+    __syncwarp();
+    barrier();
+    if (blockIdx.x % splits == 0 && threadIdx.x < 32)
+        for (int z = 1; z < splits; ++z)
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                uint32_t at;
+                float x;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(shared_address(&total[n][threadIdx.x])), "r"(z));
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
+                sum[n] += x;
+            }
+    barrier();  // the others' memory stays until it is read
+}
+// Blocks of a cluster for each of `jobs` jobs of up to `most` partial sums: two or more sums for every warp,
+// while the blocks start together (four an SM).
+inline int join_splits(long long most, long long jobs) {
+    int n = 1;
+    while (n < 8 && most > 2ll * kFinalWarps * n && 2 * n * jobs <= 4 * kSMs) n *= 2;
+    return n;
+}
+// `blocks`: a multiple of `splits`.
+template <typename... P, typename... A>
+cudaError_t launch_join(void (*kernel)(P...), long long blocks, int splits, cudaStream_t st, const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(32 * kFinalWarps);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = splits;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 }  // namespace slra
