@@ -149,10 +149,10 @@ __device__ __forceinline__ float4 join_teams(float4 u, int size, float* scratch)
 // in its part of shared memory, the former in the ring behind the row's own units, the latter behind the ring.
 // Vector v of tensor k is at unit (k V + v) u; u units of 16 bytes hold eight elements.
 struct ModWalk {
-    const char* p;
+    const char* p;         // moves on where there is no such tensor too: ask the tensor
     long long step, back;  // as RowWalk's
     __device__ ModWalk(const ModTensor& m, int size, int b, int l, int tokens)
-        : p(m.p ? static_cast<const char*>(m.p) + (b * m.b + l * m.f) * size : nullptr),
+        : p(static_cast<const char*>(m.p) + (b * m.b + l * m.f) * size),
           step(m.f * size), back((m.b - tokens * m.f) * size) {}
     __device__ __forceinline__ void next() { p += step; }
     __device__ __forceinline__ void wrap() { p += back; }
@@ -231,9 +231,9 @@ __global__ void __launch_bounds__(WIDE ? fwd_threads(V) : 128, WIDE ? 1 : kFwdNa
                 if (Y) ring.copy<SPLIT>(v * ONE + UX, py.at(c0 + v * step), gap);
                 if (TOKEN) {
                     const uint32_t m = ring.in + (U + v * MU) * ring.unit, next = V * MU * ring.unit;
-                    if (psc.p) copy_any<SPLIT>(m, ring.unit, psc.p, a.mod_dtype, c0 + v * step, gap);
-                    if (psh.p) copy_any<SPLIT>(m + next, ring.unit, psh.p, a.mod_dtype, c0 + v * step, gap);
-                    if (Y && pg.p) copy_any<SPLIT>(m + 2 * next, ring.unit, pg.p, a.mod_dtype, c0 + v * step, gap);
+                    if (a.scale.p) copy_any<SPLIT>(m, ring.unit, psc.p, a.mod_dtype, c0 + v * step, gap);
+                    if (a.shift.p) copy_any<SPLIT>(m + next, ring.unit, psh.p, a.mod_dtype, c0 + v * step, gap);
+                    if (Y && a.gate.p) copy_any<SPLIT>(m + 2 * next, ring.unit, pg.p, a.mod_dtype, c0 + v * step, gap);
                 }
             }
         }, [&]() {
@@ -456,8 +456,8 @@ __global__ void __launch_bounds__(WIDE ? bwd_threads(V) : 128, WIDE ? 1 : kBwdNa
                 if (Y) ring.copy<SPLIT>(v * ONE + YU, py.at(c0 + v * step), gap);
                 if (TOKEN) {
                     const uint32_t m = ring.in + (U + v * MU) * ring.unit;
-                    if (psc.p) copy_any<SPLIT>(m, ring.unit, psc.p, a.mod_dtype, c0 + v * step, gap);
-                    if (Y && pg.p) copy_any<SPLIT>(m + V * MU * ring.unit, ring.unit, pg.p, a.mod_dtype, c0 + v * step, gap);
+                    if (a.scale.p) copy_any<SPLIT>(m, ring.unit, psc.p, a.mod_dtype, c0 + v * step, gap);
+                    if (Y && a.gate.p) copy_any<SPLIT>(m + V * MU * ring.unit, ring.unit, pg.p, a.mod_dtype, c0 + v * step, gap);
                 }
             }
         }, [&]() {

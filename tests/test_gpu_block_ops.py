@@ -230,6 +230,58 @@ def test_norm_modulation_rows(B, L, F, C, weights):
     check_norm_backward(p, t, d)
 
 
+@pytest.mark.parametrize("stream,block", TYPES)
+@pytest.mark.parametrize("B,L,C", [(3, 4001, 72), (5, 1300, 240), (3, 1333, 392), (2, 700, 1536), (2, 307, 5120), (1, 450, 5136),
+                                   (1, 300, 8192)])
+def test_norm_modulation_for_each_token(stream, block, B, L, C):
+    """Several rows a worker with vectors of their own: rings of several stages, and rows too wide for two."""
+    for mod, weights, norm, post in ((FP, FP, slra.NORM_LAYER, slra.NORM_RMS), (block, block, slra.NORM_RMS, slra.NORM_NONE),
+                                     (block, None, slra.NORM_LAYER, slra.NORM_NONE)):
+        p, t, d = norm_inputs(B, L, C, L, stream, block, mod, weights=weights, norm=norm, post=post, rs=0.5, seed=C)
+        check_norm_forward(p, t)
+        check_norm_backward(p, t, d)
+
+
+@pytest.mark.parametrize("C", [88, 1040])
+@pytest.mark.parametrize("given", [("gate",), ("scale",), ("shift",), ("gate", "shift", "weight"), ("scale", "bias"), ("post_weight",)])
+def test_norm_some_vectors_for_each_token(C, given):
+    p, t, d = norm_inputs(2, 800, C, 800, stream=FP, weights=BF, post=slra.NORM_RMS, seed=43)
+    for n in ("gate", "scale", "shift", "weight", "bias", "post_weight"):
+        if n not in given:
+            t[n] = None
+    check_norm_forward(p, t)
+    check_norm_backward(p, t, d)
+
+
+def test_norm_vectors_for_each_token_broadcast_and_strided():
+    """Rows of a wider tensor, and one row behind every token and sample."""
+    for C in (88, 1040):
+        p, t, d = norm_inputs(3, 500, C, 500, stream=FP, weights=BF, seed=44)
+        wide = torch.randn(3, 500, 3 * C, device="cuda")
+        t["gate"], t["scale"] = wide[:, :, :C], wide[:, :, 2 * C:]
+        t["shift"] = wide[:1, :1, C:2 * C].expand(3, 500, C)
+        check_norm_forward(p, t)
+        check_norm_backward(p, t, d)
+
+
+def test_norm_without_residual_for_each_token():
+    for C in (88, 1040):
+        p, t, d = norm_inputs(2, 600, C, 600, stream=HF, block=HF, mod=HF, weights=HF, residual=False, seed=45)
+        check_norm_forward(p, t)
+        check_norm_backward(p, t, d)
+
+
+@pytest.mark.parametrize("B,L,F,C", [(1, 20000, 1, 64), (2, 9000, 3, 392), (1, 3000, 1, 1536), (1, 3000, 30, 1536), (40, 50, 1, 136),
+                                     (1, 600, 1, 5128)])
+def test_norm_many_partial_sums(B, L, F, C):
+    """Joins over one warp, a block and a cluster, of few columns and of many; twice with the same bits."""
+    p, t, d = norm_inputs(B, L, C, F, weights=FP, post=slra.NORM_RMS, seed=46)
+    one = check_norm_backward(p, t, d)
+    two = slra.residual_norm_bwd(p, **t, **d)
+    for a, b in zip(one[:8], two[:8]):
+        assert a is None or torch.equal(a, b)
+
+
 def test_norm_without_vectors():
     for given in ((), ("gate",), ("scale",), ("shift",), ("weight",), ("bias",), ("post_weight",)):
         p, t, d = norm_inputs(2, 19, 136, weights=FP, post=slra.NORM_RMS, seed=5)
