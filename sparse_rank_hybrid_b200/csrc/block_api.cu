@@ -127,10 +127,12 @@ slra_status derive(const slra_residual_norm* p, Rows* d) {
         if (!aligned16(v)) return SLRA_ERR_ALIGNMENT;
     for (const void* v : {p->dgate, p->dscale, p->dshift, p->dweight, p->dbias, p->dpost_weight})
         if (!aligned16(v)) return SLRA_ERR_ALIGNMENT;
-    const RowPlan plan = residual_norm_plan(p->batch * L, static_cast<int>(C), true);
+    const RowPlan plan = residual_norm_plan(p->batch * L, static_cast<int>(C), true,
+                                            p->post_norm != SLRA_NORM_NONE && p->tokens > p->groups);
     const size_t one = static_cast<size_t>(plan.workers) * 3 * C * sizeof(float);
     d->part = 0;
-    d->wpart = p->dgate || p->dscale || p->dshift ? align_up(2 * one, 256) : 0;
+    // nothing to join where every row has modulation vectors of its own
+    d->wpart = p->tokens > p->groups && (p->dgate || p->dscale || p->dshift) ? align_up(2 * one, 256) : 0;
     d->bytes = d->wpart + (p->dweight || p->dbias || p->dpost_weight ? align_up(one, 256) : 0);
     if (d->bytes == 0) d->bytes = 256;
     return SLRA_OK;

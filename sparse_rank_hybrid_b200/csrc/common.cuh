@@ -273,11 +273,12 @@ constexpr int kMaxWorkers = 32768;  // teams of threads that share a call's rows
 constexpr int kNormNone = 0, kNormRms = 1, kNormLayer = 2;  // slra_norm
 
 // How a call's rows are shared out: `V` vectors of eight elements a thread, `team` threads a row,
-// `workers` teams in all, in blocks of `threads` threads, worker w on rows [w share, (w + 1) share).  A row may be cut into `parts` that different blocks
-// take (`blocks` = parts times those that hold the workers).
+// `workers` teams in all, in blocks of `threads` threads, worker w on rows [w share, (w + 1) share).  A row may
+// be cut into `parts` that different blocks take (`blocks` = parts times those that hold the workers).
 struct RowPlan {
     int VQ;  // of the V vectors those that are q's (qk_rope)
     int V, team, threads, blocks, workers, share, parts;
+    bool sums;  // residual_norm_plan
 };
 
 struct RowTensor {  // [B][L][C], C contiguous; element strides of batch and token
@@ -305,7 +306,8 @@ struct ResidualNormArgs {
     // set by the launcher
     int team, teams, workers, blocks, share, stages, wsum_shared, mod_units, weight_units;
 };
-RowPlan residual_norm_plan(long long rows, int channels, bool backward);
+// `sums`: with the norm behind the block, and modulation rows of several rows
+RowPlan residual_norm_plan(long long rows, int channels, bool backward, bool sums);
 cudaError_t launch_residual_norm(const ResidualNormArgs& a, bool backward, cudaStream_t st);
 
 constexpr int kRopeMaxPairs = 128;  // head_dim <= 256

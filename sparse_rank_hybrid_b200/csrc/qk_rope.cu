@@ -11,6 +11,7 @@ __global__ void __launch_bounds__(32 * kFinalWarps) qk_rope_final_kernel(const f
     __shared__ float red[kFinalWarps][32], total[1][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x / splits * 32 + lane;
     float sum[1] = {0.f};
+    wait_for_rows();
     if (c < columns)
 #pragma unroll 8
         for (int w = warp + blockIdx.x % splits * kFinalWarps; w < workers; w += kFinalWarps * splits)

@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(WIDE ? rope_threads(VQ + VK, BWD) : 128)
     }
 
     if (!BWD || !a.part) return;
+    launch_dependents();
     const int sides = a.side[1].heads > 0 ? 2 : 1;
     if (norm == kQkNormToken) {
         float* sums = a.part + static_cast<long long>(worker) * (a.side[0].heads + a.side[1].heads) * D + c0;

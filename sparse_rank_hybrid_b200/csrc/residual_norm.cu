@@ -45,6 +45,7 @@ residual_norm_final_kernel(const __grid_constant__ ResidualNormArgs a, const Joi
         if (w0 * a.share < first) second = w0;
     }
     float sum[3] = {0.f, 0.f, 0.f};
+    wait_for_rows();
     if (in) {
         const long long row = 3ll * a.channels;
 #pragma unroll 8
@@ -88,8 +89,9 @@ residual_norm_final_kernel(const __grid_constant__ ResidualNormArgs a, const Joi
 
 }  // namespace
 
-RowPlan residual_norm_plan(long long rows, int channels, bool backward) {
+RowPlan residual_norm_plan(long long rows, int channels, bool backward, bool sums) {
     RowPlan p;
+    p.sums = sums;
     const int slots = channels / 8;
     row_team(slots, slots > 640 ? 2 : 1, &p);
     row_workers(rows, kSMs * blocks_per_sm(p, backward), &p);
@@ -98,15 +100,16 @@ RowPlan residual_norm_plan(long long rows, int channels, bool backward) {
 
 cudaError_t launch_residual_norm(const ResidualNormArgs& args, bool backward, cudaStream_t st) {
     ResidualNormArgs a = args;
-    const RowPlan p = residual_norm_plan(a.rows, a.channels, backward);
+    const RowPlan p = residual_norm_plan(a.rows, a.channels, backward, a.post != kNormNone && a.per > 1);
     a.team = p.team;
     a.workers = p.workers;
     a.share = p.share;
     a.blocks = p.blocks;
     a.teams = p.threads / p.team;
-    // A modulation row for every row: its vectors come through the ring where two rows of them fit.
+    // A modulation row for every row: its vectors come through the ring, in the backward where two rows of them
+    // fit (or other blocks' copies fill the gaps).
     const RowShared s = row_shared(a, p, backward, true);
-    const bool token = a.per == 1 && (s.stages > 1 || (s.stages == 1 && (a.share == 1 || p.team <= 32)));
+    const bool token = a.per == 1 && (s.stages > 1 || (s.stages == 1 && (!backward || a.share == 1 || p.team <= 32)));
     const cudaError_t e = backward ? (token ? launch_residual_norm_bwd_token(a, p, st) : launch_residual_norm_bwd(a, p, st))
                                    : (token ? launch_residual_norm_fwd_token(a, p, st) : launch_residual_norm_fwd(a, p, st));
     if (e != cudaSuccess || !backward) return e;

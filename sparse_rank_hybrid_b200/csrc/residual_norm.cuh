@@ -48,7 +48,10 @@ constexpr size_t kRingBytes = 200 * 1024;  // dynamic shared memory of an SM's b
 // accumulators (backward).  One vector of eight channels a thread as long as the block holds the row (5120
 // channels forward: 483 us, with two vectors and half the threads, two blocks an SM, 545), two above.
 constexpr int fwd_threads(int V) { return V == 1 ? 1024 : 640; }
-constexpr int bwd_threads(int V) { return V == 1 ? 640 : 512; }
+// Backward, with the norm behind the block (`sums`: three dependent sums a row) more warps on fewer registers hide
+// more than those cost (47,250 x 2048 affine: 298 us with 640 threads, 271 with 768; 30,990 x 2 x 2696 fp32 stream
+// 714 and 587), without it they hide less (47,250 x 2048: 204 and 222), nor with vectors for each row (683 and 873).
+constexpr int bwd_threads(int V, bool sums) { return V > 1 ? 512 : sums ? 768 : 640; }
 // Blocks an SM for rows that share a block of 128 threads.
 constexpr int kFwdNarrow = 5, kBwdNarrow = 4;
 
@@ -246,7 +249,9 @@ __global__ void __launch_bounds__(WIDE ? fwd_threads(V) : 128, WIDE ? 1 : kFwdNa
         ring.filled();
         async_commit();
     };
-    for (int s = 0; s < a.stages - 1; ++s) prefetch();
+    // A stage of rows with vectors of their own is large: filled again as soon as it is read, one more row is in
+    // flight (41,854 x 4624 fp16 with fp32 vectors: 829 -> 591 us).  Else that is slower (720p: 515 -> 555).
+    for (int s = 0; s < a.stages - (TOKEN ? 0 : 1); ++s) prefetch();
 
     Vec cg[V], ca[V], cb[V];  // gate wp, w (1 + scale), b (1 + scale) + shift
 #pragma unroll
@@ -285,7 +290,7 @@ __global__ void __launch_bounds__(WIDE ? fwd_threads(V) : 128, WIDE ? 1 : kFwdNa
         }
     };
     auto row = [&](bool valid) {
-        prefetch();
+        if (!TOKEN) prefetch();
         ring_wait(a.stages);
         Vec o[V], y[V];
 #pragma unroll
@@ -323,6 +328,7 @@ __global__ void __launch_bounds__(WIDE ? fwd_threads(V) : 128, WIDE ? 1 : kFwdNa
             }
         }
         ring.done();
+        if (TOKEN) prefetch();
         if constexpr (Y != 0) {
             if constexpr (Y == 2) {
                 float2 acc = both(0.f);
@@ -401,7 +407,7 @@ __global__ void __launch_bounds__(WIDE ? fwd_threads(V) : 128, WIDE ? 1 : kFwdNa
 }
 
 template <typename TS, typename TB, int V, int Y, bool WIDE, bool TOKEN>
-__global__ void __launch_bounds__(WIDE ? bwd_threads(V) : 128, WIDE ? 1 : kBwdNarrow) residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a) {
+__global__ void __launch_bounds__(WIDE ? bwd_threads(V, Y == 2 && !TOKEN) : 128, WIDE ? 1 : kBwdNarrow) residual_norm_bwd_kernel(const __grid_constant__ ResidualNormArgs a) {
     constexpr bool SPLIT = sizeof(TS) == 4;
     constexpr int UX = kUnits<TS>, UB = kUnits<TB>;
     // x, dx_out, dh and y of each vector
@@ -765,6 +771,7 @@ __global__ void __launch_bounds__(WIDE ? bwd_threads(V) : 128, WIDE ? 1 : kBwdNa
         });
     else
         runs<WIDE>(at, a.per, l - f * a.per, begin, row, end);
+    launch_dependents();
     if (!a.wpart || (WIDE && wsum == wslot && !TOKEN)) return;
     // A block's slot: its first worker's.
 #pragma unroll
@@ -791,7 +798,7 @@ __global__ void __launch_bounds__(WIDE ? bwd_threads(V) : 128, WIDE ? 1 : kBwdNa
 // Blocks that an SM holds at once, from the registers the kernels need.
 inline int blocks_per_sm(const RowPlan& p, bool backward) {
     if (p.team <= 32) return backward ? kBwdNarrow : kFwdNarrow;
-    return std::max(1, (backward ? bwd_threads(p.V) : fwd_threads(p.V)) / p.threads);
+    return std::max(1, (backward ? bwd_threads(p.V, p.sums) : fwd_threads(p.V)) / p.threads);
 }
 
 template <typename K>
@@ -822,7 +829,7 @@ inline RowShared row_shared(const ResidualNormArgs& a, const RowPlan& p, bool ba
         s.weight_units = !a.weight && !a.bias && !a.post_weight ? 0 : a.w_dtype == kF32 ? 2 : 1;
         units += ((backward ? 1 : 2) + y) * s.mod_units;
     }
-    s.stages = ring_stages(units * unit, per_sm, room, a.share, 1);
+    s.stages = ring_stages(units * unit, per_sm, room, a.share, 1, token && !backward);
     if (token) {  // the weights too, if the ring keeps its stages
         weights = 3 * s.weight_units * unit;
         if (s.stages * units * unit + weights > room) s.weight_units = 0, weights = 0;

@@ -370,10 +370,10 @@ inline void row_workers(long long rows, int most, RowPlan* p) {
 }
 // Stages of a ring: enough that an SM's blocks keep 96 KB of copies in flight (about twice what its share of
 // the bandwidth moves in the time a load takes), within `room` bytes a block, and no more than a worker of
-// `most` rows takes steps of `rows`.
-inline int ring_stages(size_t stage, int blocks_per_sm, size_t room, long long most, int rows) {
-    int n = 2;
-    while (n < kMaxStages && (n - 1) * stage * blocks_per_sm < 96 * 1024) ++n;
+// `most` rows takes steps of `rows`.  `early`: a stage is read at once and filled again before its arithmetic.
+inline int ring_stages(size_t stage, int blocks_per_sm, size_t room, long long most, int rows, bool early = false) {
+    int n = early ? 1 : 2;
+    while (n < kMaxStages && (n - (early ? 0 : 1)) * stage * blocks_per_sm < 96 * 1024) ++n;
     while (n > 1 && (n * stage > room || (n - 1ll) * rows >= most)) --n;
     return n;
 }
@@ -381,6 +381,10 @@ inline int ring_stages(size_t stage, int blocks_per_sm, size_t room, long long m
 // The sums of partial sums: kernels of `kFinalWarps` warps a block.  Where a job has many, the blocks of a
 // cluster share it.
 constexpr int kFinalWarps = 16;
+
+// The joining kernel's blocks start while the row kernel's last ones end, and wait for all it has written.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_rows() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Adds the totals of the cluster's other blocks to warp 0's `sum` in its first block, in the blocks' order.
 template <int N>
@@ -416,12 +420,14 @@ cudaError_t launch_join(void (*kernel)(P...), long long blocks, int splits, cuda
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(32 * kFinalWarps);
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = splits;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
