@@ -128,7 +128,8 @@ slra_status derive(const slra_residual_norm* p, Rows* d) {
     for (const void* v : {p->dgate, p->dscale, p->dshift, p->dweight, p->dbias, p->dpost_weight})
         if (!aligned16(v)) return SLRA_ERR_ALIGNMENT;
     const RowPlan plan = residual_norm_plan(p->batch * L, static_cast<int>(C), true,
-                                            p->post_norm != SLRA_NORM_NONE && p->tokens > p->groups);
+                                            p->post_norm != SLRA_NORM_NONE, p->tokens == p->groups,
+                                            p->stream_dtype != SLRA_DTYPE_F32);
     const size_t one = static_cast<size_t>(plan.workers) * 3 * C * sizeof(float);
     d->part = 0;
     // nothing to join where every row has modulation vectors of its own

@@ -306,8 +306,8 @@ struct ResidualNormArgs {
     // set by the launcher
     int team, teams, workers, blocks, share, stages, wsum_shared, mod_units, weight_units;
 };
-// `sums`: with the norm behind the block, and modulation rows of several rows
-RowPlan residual_norm_plan(long long rows, int channels, bool backward, bool sums);
+// `post`: the norm behind the block; `token`: a modulation row for each row; `half`: all rows in 16 bits
+RowPlan residual_norm_plan(long long rows, int channels, bool backward, bool post, bool token, bool half);
 cudaError_t launch_residual_norm(const ResidualNormArgs& a, bool backward, cudaStream_t st);
 
 constexpr int kRopeMaxPairs = 128;  // head_dim <= 256

@@ -89,27 +89,31 @@ residual_norm_final_kernel(const __grid_constant__ ResidualNormArgs a, const Joi
 
 }  // namespace
 
-RowPlan residual_norm_plan(long long rows, int channels, bool backward, bool sums) {
+RowPlan residual_norm_plan(long long rows, int channels, bool backward, bool post, bool token, bool half) {
     RowPlan p;
-    p.sums = sums;
+    p.sums = post && !token;
     const int slots = channels / 8;
-    row_team(slots, slots > 640 ? 2 : 1, &p);
+    // Two vectors a thread above 5120 channels.  In the backward also where two blocks an SM then hold the rows that
+    // only one would else, with 16-bit rows and enough of them (all us, one vector and two): 11,575 x 5 x 3344 with
+    // the norm behind the block 756 and 569, 12,665 x 5 x 3056 without 484 and 413, 25,043 x 2 x 3864 with vectors for
+    // each token 2220 and 1664.  Not so few rows (1010 x 5 x 2712: 67 and 79), vectors for each token without the norm
+    // behind the block (21,853 x 3 x 2952: 1443 and 1719), or an fp32 stream (2900 x 3640: 80 and 90).
+    const bool pairs = backward && half && (post || !token) && rows >= 40 * kSMs && slots <= 512 &&
+                       slots > bwd_threads(1, p.sums) / 2;
+    row_team(slots, slots > 640 || pairs ? 2 : 1, &p);
     row_workers(rows, kSMs * blocks_per_sm(p, backward), &p);
     return p;
 }
 
 cudaError_t launch_residual_norm(const ResidualNormArgs& args, bool backward, cudaStream_t st) {
     ResidualNormArgs a = args;
-    const RowPlan p = residual_norm_plan(a.rows, a.channels, backward, a.post != kNormNone && a.per > 1);
+    const RowPlan p = residual_norm_plan(a.rows, a.channels, backward, a.post != kNormNone, a.per == 1, a.stream_dtype != kF32);
     a.team = p.team;
     a.workers = p.workers;
     a.share = p.share;
     a.blocks = p.blocks;
     a.teams = p.threads / p.team;
-    // A modulation row for every row: its vectors come through the ring, in the backward where two rows of them
-    // fit (or other blocks' copies fill the gaps).
-    const RowShared s = row_shared(a, p, backward, true);
-    const bool token = a.per == 1 && (s.stages > 1 || (s.stages == 1 && (!backward || a.share == 1 || p.team <= 32)));
+    const bool token = a.per == 1;  // a modulation row for each row
     const cudaError_t e = backward ? (token ? launch_residual_norm_bwd_token(a, p, st) : launch_residual_norm_bwd(a, p, st))
                                    : (token ? launch_residual_norm_fwd_token(a, p, st) : launch_residual_norm_fwd(a, p, st));
     if (e != cudaSuccess || !backward) return e;

@@ -27,8 +27,8 @@
 // Where every row has its own modulation vectors (TOKEN: per-token modulation, single tokens) those would be
 // loaded and waited for in each row: they travel through the ring with it instead, their gradients are written
 // as the row is, and the accumulators hold the weights' sums (60,983 x 392 with an fp32 stream and affine norm,
-// backward: 676 -> 189 us; 18,550 x 3 x 1128 in fp32: 1555 -> 677; 7716 x 5 x 5016 forward: 841 -> 597).  A
-// ring that then has one stage is worse than waiting, except where several blocks of narrow rows share the SM.
+// backward: 676 -> 189 us; 18,550 x 3 x 1128 in fp32: 1555 -> 677; 7716 x 5 x 5016 forward: 841 -> 597), even
+// where the ring then has one stage only.  One stage of the widest rows, all in fp32, always fits (192 KB).
 //
 // B200, back to back, against 6557 GB/s of copy rate: 75,600 x 5120 bf16 forward 0.48-0.52 ms (92-98%),
 // backward 0.73-0.79 ms (90-97%); 32,760 x 1536 with an fp32 stream forward 109 us (85%), backward with
@@ -837,7 +837,6 @@ inline RowShared row_shared(const ResidualNormArgs& a, const RowPlan& p, bool ba
     // the sums take what the ring leaves
     if (backward && !token && a.wpart && (s.stages * units + 6) * unit <= room) s.wsum = 1, weights = 6 * unit;
     s.bytes = s.stages * units * unit + weights;
-    if (s.bytes > room) s.stages = 0;
     return s;
 }
 

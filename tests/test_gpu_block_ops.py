@@ -242,6 +242,15 @@ def test_norm_modulation_for_each_token(stream, block, B, L, C):
         check_norm_backward(p, t, d)
 
 
+@pytest.mark.parametrize("F", [1, 5930])
+@pytest.mark.parametrize("C", [2568, 3336, 4096])
+def test_norm_two_vectors_a_thread(C, F):
+    """Many 16-bit rows of about half a block's channels."""
+    for post in (slra.NORM_NONE, slra.NORM_RMS):
+        p, t, d = norm_inputs(1, 5930, C, F, HF, HF, HF, weights=FP, post=post, seed=47)
+        check_norm_backward(p, t, d)
+
+
 @pytest.mark.parametrize("C", [88, 1040])
 @pytest.mark.parametrize("given", [("gate",), ("scale",), ("shift",), ("gate", "shift", "weight"), ("scale", "bias"), ("post_weight",)])
 def test_norm_some_vectors_for_each_token(C, given):
