@@ -32,10 +32,8 @@ __global__ void __launch_bounds__(32 * kFinalWarps) qk_rope_final_kernel(const f
     }
 }
 
-// Threads of a head.  The norm per head sums over them by exchanges in a warp; else no more than it has vectors
-// (heads of 80 then idle no thread in three).
-int group_of(int head_dim, int norm) {
-    if (norm != kQkNormHead) return head_dim / 8;
+// Threads of a head, rounded up to what a warp's exchanges sum over.
+int even_group(int head_dim) {
     int g = 1;
     while (g * 8 < head_dim) g *= 2;
     return g;
@@ -48,41 +46,52 @@ int group_of(int head_dim, int norm) {
 // 367 and 393 (apart 504).
 struct RopePlan {
     RowPlan rows;
-    int split_sides, part_heads[2];
+    int group, split_sides, part_heads[2];
 };
 
 RopePlan plan_of(long long rows, int head_dim, int q_heads, int k_heads, int norm, bool backward) {
     RopePlan best;
-    const int G = group_of(head_dim, norm);
     long long least = -1;
-    // parts of the heads, or sides apart (parts 0); vectors a thread of q and of k, or of the side
-    for (int parts = 0; parts <= 16; ++parts) {
-        if ((norm == kQkNormToken && parts > 1) || (parts == 0 && !k_heads)) continue;
-        const int hq = parts ? (q_heads + parts - 1) / parts : std::max(q_heads, k_heads);
-        const int hk = parts ? (k_heads + parts - 1) / parts : 0;
-        for (int vq = 1; vq <= 2; ++vq) {
-            RopePlan c;
-            RowPlan& p = c.rows;
-            row_team(std::max((hq * G + vq - 1) / vq, hk * G), 1, &p);
-            p.VQ = vq;
-            p.V = vq + (hk ? 1 : 0);
-            if ((vq > 1 && p.team % G != 0) || p.threads > rope_threads(p.V, backward) || (p.team <= 32 && vq > 1)) continue;
-            // Thread-steps of a row: a step costs about as much as one vector besides its vectors, and an
-            // entry of the table as much as another; registers that a thread needs are threads that the SM
-            // lacks.  Sides apart cost both blocks the table, and leave threads idle where they are unequal.
-            const int registers[2][4] = {{0, 80, 96, 128}, {0, 96, 120, 168}};
-            const int steps = backward && p.V > 1 ? 2 : 1;
-            const int shares = parts ? parts : 2 * std::min(q_heads, k_heads) < std::max(q_heads, k_heads) ? 3 : 2;
-            const long long cost = static_cast<long long>((2 * p.V + steps) * p.team + head_dim) *
-                                   registers[backward][p.V] * shares;
-            if (least >= 0 && cost >= least) continue;
-            least = cost;
-            c.split_sides = parts == 0;
-            c.part_heads[0] = hq;
-            c.part_heads[1] = parts ? hk : hq;
-            p.parts = parts ? parts : 2;
-            best = c;
+    // Threads of a head: as many as it has vectors, so that heads of 80 idle no thread in three, if no norm per head
+    // sums over them; else, or where a thread's second vector would not then be at the same place of its head, a
+    // power of two.
+    for (int G = norm == kQkNormHead ? even_group(head_dim) : head_dim / 8;; G = even_group(head_dim)) {
+        // parts of the heads, or sides apart (parts 0); vectors a thread of q and of k, or of the side
+        for (int parts = 0; parts <= 16; ++parts) {
+            if ((norm == kQkNormToken && parts > 1) || (parts == 0 && !k_heads)) continue;
+            const int hq = parts ? (q_heads + parts - 1) / parts : std::max(q_heads, k_heads);
+            const int hk = parts ? (k_heads + parts - 1) / parts : 0;
+            for (int vq = 1; vq <= 2; ++vq) {
+                RopePlan c;
+                RowPlan& p = c.rows;
+                row_team(std::max((hq * G + vq - 1) / vq, hk * G), 1, &p);
+                p.VQ = vq;
+                p.V = vq + (hk ? 1 : 0);
+                if ((vq > 1 && p.team % G != 0) || p.threads > rope_threads(p.V, backward) || (p.team <= 32 && vq > 1)) continue;
+                // Thread-steps of a row: a step costs about as much as two vectors besides its vectors (three with one
+                // token a step), and an entry of the table as much as one; times the registers that a thread takes from
+                // the SM, between what it needs and its share where the blocks leave some over (the needs alone: 90
+                // drawn calls 6% slower, 21,881 x 2 tokens of 23 + 23 heads backward 525 us for 353; the shares alone 1%
+                // slower, 32,760 tokens of 12 + 12 heads forward 107 us for 79).  Sides apart cost both blocks the
+                // table, and leave threads idle where they are unequal.
+                const int needed[2][4] = {{0, 80, 96, 128}, {0, 96, 120, 168}};
+                const int blocks = rope_blocks_per_sm(p, backward, norm != kQkNormNone);
+                const int registers = needed[backward][p.V] + 65536 / (blocks * p.threads);
+                const int steps = backward && p.V > 1 ? 3 : 2;
+                const int shares = parts ? parts : 2 * std::min(q_heads, k_heads) < std::max(q_heads, k_heads) ? 3 : 2;
+                const long long cost = static_cast<long long>((2 * p.V + steps) * p.team + head_dim) *
+                                       registers * shares;
+                if (least >= 0 && cost >= least) continue;
+                least = cost;
+                c.group = G;
+                c.split_sides = parts == 0;
+                c.part_heads[0] = hq;
+                c.part_heads[1] = parts ? hk : hq;
+                p.parts = parts ? parts : 2;
+                best = c;
+            }
         }
+        if (G == even_group(head_dim)) break;
     }
     RowPlan& p = best.rows;
     const int parts = p.parts;
@@ -106,7 +115,7 @@ cudaError_t launch_qk_rope(const QkRopeArgs& args, bool backward, cudaStream_t s
     a.split_sides = plan.split_sides;
     a.part_heads[0] = plan.part_heads[0];
     a.part_heads[1] = plan.part_heads[1];
-    a.group = group_of(a.head_dim, a.norm);
+    a.group = plan.group;
     a.team = p.team;
     a.workers = p.workers;
     a.share = p.share;

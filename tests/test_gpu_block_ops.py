@@ -597,6 +597,16 @@ def test_rope_sizes(norm, pairing, B, L, hq, hk, D):
     check_rope(p, t, d)
 
 
+@pytest.mark.parametrize("norm", NORMS)
+@pytest.mark.parametrize("hq,hk,D", [(55, 55, 96), (55, 7, 96), (64, 64, 80), (61, 1, 104), (31, 31, 248), (27, 3, 216), (9, 9, 72), (3, 1, 40), (1, 1, 24),
+                                     (33, 8, 80), (12, 0, 96)])
+def test_rope_heads_that_are_no_power_of_two(norm, hq, hk, D):
+    """A thread for each vector of a head, or more where the block's threads do not divide into heads."""
+    for pairing in (slra.ROPE_INTERLEAVED, slra.ROPE_HALVES):
+        p, t, d = rope_inputs(1, 320, hq, hk, D, norm=norm, seed=hq + D, pairing=pairing, grid=(2, 16, 10), theta=1e4)
+        check_rope(p, t, d)
+
+
 @pytest.mark.parametrize("x,out", [(BF, BF), (HF, HF), (FP, FP), (BF, FP), (HF, FP)])
 @pytest.mark.parametrize("norm", NORMS)
 @pytest.mark.parametrize("pairing", [slra.ROPE_INTERLEAVED, slra.ROPE_HALVES])
