@@ -186,7 +186,8 @@ def _own_residual_norm(s, c):
                           post_norm=kinds[c["post"]], residual_scale=c["residual_scale"])
     vectors = {n: s[n] for n in ("gate", "scale", "shift", "weight", "bias", "post_weight")}
     if c["direction"] == "fwd":
-        x_out, h = slra.residual_norm_fwd(p, s["x"], s["y"], **vectors)
+        # without a residual there is no y to give h its type
+        x_out, h = slra.residual_norm_fwd(p, s["x"], s["y"], h_dtype=None if c["residual"] else _TYPES[c["block"]], **vectors)
         return [x_out, h] if c["residual"] else [h]
     g = slra.residual_norm_bwd(p, s["x"], s["y"], dh=s["dh"], dx_out=s["dx_out"], **vectors)
     return [t for t in (g.dx, g.dy, g.dgate, g.dscale, g.dshift, g.dweight, g.dbias, g.dpost_weight) if t is not None]
