@@ -32,7 +32,7 @@
 //
 // B200, back to back, against 6557 GB/s of copy rate: 75,600 x 5120 bf16 forward 0.48-0.52 ms (92-98%),
 // backward 0.73-0.79 ms (90-97%); 32,760 x 1536 with an fp32 stream forward 109 us (85%), backward with
-// a modulation row per frame and an affine norm 192 us (72%, of which the joining launch takes 10-20).
+// a modulation row per frame and an affine norm 184-189 us (73-75%).
 #pragma once
 
 #include <algorithm>

@@ -1,4 +1,4 @@
-// Helpers of the row kernels (residual_norm.cu, qk_rope.cu): typed vectors of eight elements, each
+// Helpers of the row kernels (residual_norm.cuh, qk_rope.cuh): typed vectors of eight elements, each
 // thread's own ring of asynchronous loads, and sums over the threads that share a row.
 //
 // These kernels move few bytes per element and are bound by memory only while they issue few enough
