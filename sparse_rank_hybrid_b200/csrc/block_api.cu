@@ -258,7 +258,7 @@ slra_status derive(const slra_qk_rope* p, Heads* d) {
     a.side[1].heads = static_cast<int>(p->kv_heads);
     a.side[0].weight = p->wq;
     a.side[1].weight = p->wk;
-    a.H = a.W = 1;  // without a rotation every angle is zero
+    a.H = a.W = 1;  // without a rotation no pair has an angle
     a.halves = p->pairing == SLRA_ROPE_HALVES;
     a.norm = p->norm;
     a.x_dtype = p->x_dtype;
@@ -293,6 +293,8 @@ slra_status derive(const slra_qk_rope* p, Heads* d) {
                 a.axis[j] = static_cast<uint8_t>(ax);
             }
         }
+        const bool every = j == c && std::all_of(a.turns, a.turns + j, [](uint64_t t) { return t != 0; });
+        a.rotated = every ? kRopeAll : kRopeSome;
         a.positions = p->positions;
         a.positions_b = p->positions_stride;
         a.first = p->first_token;

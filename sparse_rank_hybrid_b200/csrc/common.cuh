@@ -312,6 +312,7 @@ cudaError_t launch_residual_norm(const ResidualNormArgs& a, bool backward, cudaS
 
 constexpr int kRopeMaxPairs = 128;  // head_dim <= 256
 constexpr int kQkNormNone = 0, kQkNormHead = 1, kQkNormToken = 2;  // slra_qk_norm
+constexpr int kRopeNone = 0, kRopeSome = 1, kRopeAll = 2;  // of a head's pairs, those that are rotated
 
 // One of q, k: its head vectors [B][L][heads][D], their counterparts and the norm's weight.
 struct RopeSide {
@@ -333,7 +334,7 @@ struct QkRopeArgs {
     int tokens, head_dim;
     int H, W;                  // grid
     long long offset[3];
-    int halves, norm;
+    int halves, norm, rotated;
     int x_dtype, out_dtype, w_dtype;
     float eps;
     float* part;  // the weights' sums (null: none is wanted): norm over a token's heads [workers][heads * D of

@@ -119,10 +119,12 @@ cudaError_t launch_qk_rope(const QkRopeArgs& args, bool backward, cudaStream_t s
     a.team = p.team;
     a.workers = p.workers;
     a.share = p.share;
-    const cudaError_t e = !backward                ? launch_qk_rope_fwd(a, p, st)
-                          : a.norm == kQkNormNone  ? launch_qk_rope_bwd_none(a, p, st)
-                          : a.norm == kQkNormHead  ? launch_qk_rope_bwd_head(a, p, st)
-                                                   : launch_qk_rope_bwd_token(a, p, st);
+    const bool all = a.rotated == kRopeAll;
+    const auto launch = !backward               ? (all ? launch_qk_rope_fwd : launch_qk_rope_fwd_some)
+                        : a.norm == kQkNormNone ? (all ? launch_qk_rope_bwd_none : launch_qk_rope_bwd_none_some)
+                        : a.norm == kQkNormHead ? (all ? launch_qk_rope_bwd_head : launch_qk_rope_bwd_head_some)
+                                                : (all ? launch_qk_rope_bwd_token : launch_qk_rope_bwd_token_some);
+    const cudaError_t e = launch(a, p, st);
     if (e != cudaSuccess || !backward || !a.part) return e;
     const bool each = a.norm == kQkNormToken;  // a weight of its own for each head
     const int q_columns = a.head_dim * (each ? a.side[0].heads : 1);
@@ -132,10 +134,6 @@ cudaError_t launch_qk_rope(const QkRopeArgs& args, bool backward, cudaStream_t s
     const int splits = join_splits(workers, (columns + 31) / 32);
     return launch_join(qk_rope_final_kernel, (columns + 31ll) / 32 * splits, splits, st, a.part, workers, columns, q_columns,
                        a.side[0].dweight, a.side[1].dweight, splits);
-}
-
-cudaError_t launch_qk_rope_fwd(const QkRopeArgs& a, const RowPlan& p, cudaStream_t st) {
-    return rope_launch_all<false, -1>(a, p, st);
 }
 
 }  // namespace slra

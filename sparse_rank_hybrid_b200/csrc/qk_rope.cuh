@@ -13,8 +13,9 @@
 // of a turn wraps around at whole turns by itself, so its upper half is the fraction of a turn to 2^-32
 // wherever the position is, for three integer multiplications (a double product with its rounding to a whole
 // number took most of the time of a step).  The table of a step's cos and sin is filled during the step
-// before it.  Without a rotation every angle is zero, which changes no bits of finite values.  Rows travel
-// through a per-thread ring of asynchronous copies as in residual_norm.cu.
+// before it.  Pairs that are not rotated pass through as they are: a product with (1, 0) would make NaN of an
+// infinity's partner and lose the sign of zeros.  Rows travel through a per-thread ring of asynchronous copies
+// (rows.cuh).
 //
 // B200, back to back, against 6557 GB/s of copy rate: 75,600 tokens x 2 x 40 heads of 128, bf16, norm per
 // head: forward 0.48-0.51 ms (93-98%), backward 0.86-0.87 ms (81-82%); 32,760 x 2 x 12 heads, norm over the
@@ -44,6 +45,10 @@ constexpr int kRows = BWD && V > 1 ? 1 : 2;
 constexpr int rope_threads(int V, bool backward) {
     return V == 1 ? 640 : V == 2 ? (backward ? 512 : 640) : (backward ? 320 : 512);
 }
+// Blocks of that many threads (narrow: of 128) that an SM has to hold.  The backward without a norm, a rotation
+// alone, needs 48 to 64 registers a thread; with the choice of rotate_some the compiler would take up to 82 (0: as it
+// sees fit).
+constexpr int rope_blocks(int V, bool wide, bool choice) { return !choice ? 0 : !wide ? 8 : V == 3 ? 3 : 2; }
 
 // The four pairs of a vector turned by their angles; the cos and sin of pairs (0, 1) and (2, 3) in c, s.
 template <bool HALVES>
@@ -65,13 +70,36 @@ __device__ __forceinline__ void rotate(Vec& v, const float2 (&c)[2], const float
     }
 }
 
+// The cosine that the tables hold for a pair that is not rotated.
+constexpr float kUnrotated = 2.f;
+
+// As `rotate`, where some of the calls' pairs are not rotated.
+template <bool HALVES>
+__device__ __forceinline__ void rotate_some(Vec& v, const float2 (&c)[2], const float2 (&s)[2]) {
+    const Vec u = v;
+    rotate<HALVES>(v, c, s);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {  // the pair's cosine and its two elements
+        const float cc = m & 1 ? c[m / 2].y : c[m / 2].x;
+        if (cc != kUnrotated) continue;
+        if constexpr (HALVES) {
+            if (m & 1) v.f[m / 2].y = u.f[m / 2].y, v.f[m / 2 + 2].y = u.f[m / 2 + 2].y;
+            else v.f[m / 2].x = u.f[m / 2].x, v.f[m / 2 + 2].x = u.f[m / 2 + 2].x;
+        } else {
+            v.f[m] = u.f[m];
+        }
+    }
+}
+
 // A vector is eight consecutive elements of a head, or four of each half (SPLIT): where the halves are paired,
 // and where a tensor is fp32, so that a warp's accesses cover consecutive memory (480p backward from fp32
 // gradients: 197 -> 146 us).  Of a thread's vectors VQ are of q and VK of k; without the latter they are of
 // the side that the block takes.
-template <typename TX, typename TO, int VQ, int VK, bool HALVES, bool BWD, bool WIDE, int NORM>
-__global__ void __launch_bounds__(WIDE ? rope_threads(VQ + VK, BWD) : 128)
+template <typename TX, typename TO, int VQ, int VK, bool HALVES, bool BWD, bool WIDE, int NORM, bool ALL>
+__global__ void __launch_bounds__(WIDE ? rope_threads(VQ + VK, BWD) : 128,
+                                  rope_blocks(VQ + VK, WIDE, BWD && NORM == kQkNormNone && !ALL))
     qk_rope_kernel(const __grid_constant__ QkRopeArgs a) {
+    // ALL: every pair is rotated.  Compiled apart: the choice at run time costs those calls up to 3%.
     // The backward is compiled for each norm: it issues so many instructions that the choice at run time
     // costs it a fifth (720p, norm per head: 1014 -> 861 us); the forward does not notice.
     const int norm = NORM < 0 ? a.norm : NORM;
@@ -178,6 +206,7 @@ __global__ void __launch_bounds__(WIDE ? rope_threads(VQ + VK, BWD) : 128)
             float sn, c;  // of the signed fraction in half turns
             sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f, &sn, &c);
             float* cs = table + (which * R + r) * 2 * pairs;
+            if (!ALL && turns[j] == 0) c = kUnrotated;
             cs[j] = c;
             cs[pairs + j] = BWD ? -sn : sn;  // the gradient turns back
         }
@@ -185,6 +214,11 @@ __global__ void __launch_bounds__(WIDE ? rope_threads(VQ + VK, BWD) : 128)
     };
     if (n > 0) fill(0, n);
     team.sync();
+
+    auto turn = [&](Vec& v, int r, const float2 (&c)[R][2], const float2 (&sn)[R][2]) {
+        if (ALL) rotate<HALVES>(v, c[r], sn[r]);
+        else if (a.rotated == kRopeSome) rotate_some<HALVES>(v, c[r], sn[r]);
+    };
 
     const float inv_head = 1.0f / D;
     const float inv_q = 1.0f / (static_cast<float>(D) * a.side[side_q].heads);
@@ -222,7 +256,7 @@ __global__ void __launch_bounds__(WIDE ? rope_threads(VQ + VK, BWD) : 128)
                 if (need_x) x[r][v] = ring.read<TX>((r * V + v) * ONE);
                 if (BWD) {
                     g[r][v] = ring.read<TO>((r * V + v) * ONE + UX);
-                    rotate<HALVES>(g[r][v], c[r], sn[r]);
+                    turn(g[r][v], r, c, sn);
                 }
             }
         ring.done();
@@ -296,7 +330,7 @@ __global__ void __launch_bounds__(WIDE ? rope_threads(VQ + VK, BWD) : 128)
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 x[r][v].f[e] = mul2(x[r][v].f[e], mul2(w[v].f[e], both(rd[r][v])));
-                        rotate<HALVES>(x[r][v], c[r], sn[r]);
+                        turn(x[r][v], r, c, sn);
                         if (on[v]) store_vec<TW, SPLIT>(out, x[r][v], gap);
                     } else {
                         if (norm) {
@@ -365,7 +399,7 @@ inline int rope_blocks_per_sm(const RowPlan& p, bool backward, bool norm) {
     return std::max(1, warps * 32 / p.threads);
 }
 
-template <typename TX, typename TO, int VQ, int VK, bool HALVES, bool BWD, bool WIDE, int NORM>
+template <typename TX, typename TO, int VQ, int VK, bool HALVES, bool BWD, bool WIDE, int NORM, bool ALL>
 cudaError_t rope_launch(QkRopeArgs a, const RowPlan& p, cudaStream_t st) {
     for (RopeSide& s : a.side) {
         const long long x = sizeof(TX), d = sizeof(TO), o = BWD ? sizeof(TX) : sizeof(TO);
@@ -378,7 +412,7 @@ cudaError_t rope_launch(QkRopeArgs a, const RowPlan& p, cudaStream_t st) {
     const int per_sm = rope_blocks_per_sm(p, BWD, a.norm != kQkNormNone);
     a.stages = ring_stages(stage, per_sm, kRopeRingBytes / per_sm, a.share, R);
     const size_t smem = a.stages * stage + size_t(p.threads / p.team) * 2 * R * a.head_dim * sizeof(float);
-    const auto kernel = qk_rope_kernel<TX, TO, VQ, VK, HALVES, BWD, WIDE, NORM>;
+    const auto kernel = qk_rope_kernel<TX, TO, VQ, VK, HALVES, BWD, WIDE, NORM, ALL>;
     if (smem > 40 * 1024) {  // 48 KB without opting in, less the static part
         const cudaError_t e =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -387,13 +421,13 @@ cudaError_t rope_launch(QkRopeArgs a, const RowPlan& p, cudaStream_t st) {
     kernel<<<p.blocks, p.threads, smem, st>>>(a);
     return cudaGetLastError();
 }
-template <typename TX, typename TO, bool BWD, int NORM>
+template <typename TX, typename TO, bool BWD, int NORM, bool ALL>
 cudaError_t rope_launch_types(const QkRopeArgs& a, const RowPlan& p, cudaStream_t st) {
     const auto shape = [&](auto vq, auto vk, auto wide) {
         constexpr int VQ = decltype(vq)::value, VK = decltype(vk)::value;
         constexpr bool WIDE = decltype(wide)::value;
-        return a.halves ? rope_launch<TX, TO, VQ, VK, true, BWD, WIDE, NORM>(a, p, st)
-                        : rope_launch<TX, TO, VQ, VK, false, BWD, WIDE, NORM>(a, p, st);
+        return a.halves ? rope_launch<TX, TO, VQ, VK, true, BWD, WIDE, NORM, ALL>(a, p, st)
+                        : rope_launch<TX, TO, VQ, VK, false, BWD, WIDE, NORM, ALL>(a, p, st);
     };
     const std::integral_constant<int, 0> none;
     const std::integral_constant<int, 1> one;
@@ -404,19 +438,24 @@ cudaError_t rope_launch_types(const QkRopeArgs& a, const RowPlan& p, cudaStream_
     return k ? shape(two, one, std::true_type()) : shape(two, none, std::true_type());
 }
 
-// The kernels of one direction and norm (NORM -1: any), each in a file of its own.
-template <bool BWD, int NORM>
+// The kernels of one direction and norm (NORM -1: any), for calls that rotate every pair (ALL) and for the others,
+// each in a file of its own.
+template <bool BWD, int NORM, bool ALL>
 cudaError_t rope_launch_all(const QkRopeArgs& a, const RowPlan& p, cudaStream_t st) {
-    if (a.x_dtype == kF32) return rope_launch_types<float, float, BWD, NORM>(a, p, st);
+    if (a.x_dtype == kF32) return rope_launch_types<float, float, BWD, NORM, ALL>(a, p, st);
     if (a.x_dtype == kBf16)
-        return a.out_dtype == kF32 ? rope_launch_types<__nv_bfloat16, float, BWD, NORM>(a, p, st)
-                                   : rope_launch_types<__nv_bfloat16, __nv_bfloat16, BWD, NORM>(a, p, st);
-    return a.out_dtype == kF32 ? rope_launch_types<__half, float, BWD, NORM>(a, p, st)
-                               : rope_launch_types<__half, __half, BWD, NORM>(a, p, st);
+        return a.out_dtype == kF32 ? rope_launch_types<__nv_bfloat16, float, BWD, NORM, ALL>(a, p, st)
+                                   : rope_launch_types<__nv_bfloat16, __nv_bfloat16, BWD, NORM, ALL>(a, p, st);
+    return a.out_dtype == kF32 ? rope_launch_types<__half, float, BWD, NORM, ALL>(a, p, st)
+                               : rope_launch_types<__half, __half, BWD, NORM, ALL>(a, p, st);
 }
 cudaError_t launch_qk_rope_fwd(const QkRopeArgs& a, const RowPlan& p, cudaStream_t st);
 cudaError_t launch_qk_rope_bwd_none(const QkRopeArgs& a, const RowPlan& p, cudaStream_t st);
 cudaError_t launch_qk_rope_bwd_head(const QkRopeArgs& a, const RowPlan& p, cudaStream_t st);
 cudaError_t launch_qk_rope_bwd_token(const QkRopeArgs& a, const RowPlan& p, cudaStream_t st);
+cudaError_t launch_qk_rope_fwd_some(const QkRopeArgs& a, const RowPlan& p, cudaStream_t st);
+cudaError_t launch_qk_rope_bwd_none_some(const QkRopeArgs& a, const RowPlan& p, cudaStream_t st);
+cudaError_t launch_qk_rope_bwd_head_some(const QkRopeArgs& a, const RowPlan& p, cudaStream_t st);
+cudaError_t launch_qk_rope_bwd_token_some(const QkRopeArgs& a, const RowPlan& p, cudaStream_t st);
 
 }  // namespace slra

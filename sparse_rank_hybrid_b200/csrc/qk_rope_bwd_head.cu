@@ -4,7 +4,7 @@
 namespace slra {
 
 cudaError_t launch_qk_rope_bwd_head(const QkRopeArgs& a, const RowPlan& p, cudaStream_t st) {
-    return rope_launch_all<true, kQkNormHead>(a, p, st);
+    return rope_launch_all<true, kQkNormHead, true>(a, p, st);
 }
 
 }  // namespace slra

@@ -1,0 +1,10 @@
+// The backward kernels of qk_rope.cuh with a norm over a token's heads, not every pair rotated.
+#include "qk_rope.cuh"
+
+namespace slra {
+
+cudaError_t launch_qk_rope_bwd_token_some(const QkRopeArgs& a, const RowPlan& p, cudaStream_t st) {
+    return rope_launch_all<true, kQkNormToken, false>(a, p, st);
+}
+
+}  // namespace slra

@@ -1,0 +1,10 @@
+// QK norm and rotary positions: forward, not every pair rotated (qk_rope.cuh).
+#include "qk_rope.cuh"
+
+namespace slra {
+
+cudaError_t launch_qk_rope_fwd_some(const QkRopeArgs& a, const RowPlan& p, cudaStream_t st) {
+    return rope_launch_all<false, -1, false>(a, p, st);
+}
+
+}  // namespace slra

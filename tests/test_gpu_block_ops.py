@@ -879,3 +879,73 @@ def test_block_half_with_the_attention():
     dh0 = (dqkv.view(B, L, 3 * C) @ wqkv)
     t0 = dict(x=x, y=None, gate=None, scale=mods["scale0"], shift=mods["shift0"], weight=None, bias=None, post_weight=None)
     check_norm_backward(first, t0, dict(dh=dh0, dx_out=last.dx))
+
+
+def unrotated(D, split, pairing):
+    """Mask [D] of the elements that a split leaves alone."""
+    j = torch.arange(D, device="cuda")
+    pair = j % (D // 2) if pairing == slra.ROPE_HALVES else j // 2
+    return pair >= sum(split)
+
+
+def same_bits(a, b):
+    ints = {2: torch.int16, 4: torch.int32}[a.element_size()]
+    return torch.equal(a.contiguous().view(ints), b.contiguous().view(ints))
+
+
+@pytest.mark.parametrize("x,out", [(BF, BF), (HF, HF), (FP, FP), (BF, FP)])
+@pytest.mark.parametrize("pairing", [slra.ROPE_INTERLEAVED, slra.ROPE_HALVES])
+@pytest.mark.parametrize("D,split", [(64, (3, 0, 5)), (128, (1, 0, 0)), (40, (7, 6, 6)), (8, (0, 2, 0))])
+def test_rope_pairs_that_are_not_rotated_pass_through(x, out, pairing, D, split):
+    """Their bits arrive as they are, forward and backward: infinities, NaN and zeros of either sign, which a
+    product with (1, 0) would spread to the pair's other element or lose."""
+    code = {BF: slra.DTYPE_BF16, HF: slra.DTYPE_F16, FP: slra.DTYPE_F32}[out]
+    for hq, hk in ((3, 1), (20, 20)):
+        p, t, d = rope_inputs(2, 33, hq, hk, D, x, out, norm=slra.QK_NORM_NONE, pairing=pairing, rope_split=split, grid=(3, 4, 3),
+                              out_dtype=code, seed=50)
+        keep = unrotated(D, split, pairing)
+        special = torch.tensor([float("inf"), -float("inf"), float("nan"), -0.0, 0.0], device="cuda")
+        for v in (t["q"], t["k"], d["dout_q"], d["dout_k"]):
+            at = (torch.rand(v.shape, device="cuda", generator=torch.Generator("cuda").manual_seed(51)) < 0.2) & keep
+            v[at] = special[torch.arange(int(at.sum()), device="cuda") % 5].to(v.dtype)
+        clean = {n: None if v is None else torch.where(keep, torch.ones_like(v), v) for n, v in t.items()}
+        cleand = {n: torch.where(keep, torch.ones_like(v), v) for n, v in d.items()}
+        outs, ref = slra.qk_rope_fwd(p, **t), slra.qk_rope_fwd(p, **clean)
+        got, gref = slra.qk_rope_bwd(p, t["q"], t["k"], **d), slra.qk_rope_bwd(p, clean["q"], clean["k"], **cleand)
+        for o, r, v in ((outs[0], ref[0], t["q"]), (outs[1], ref[1], t["k"]), (got.dq, gref.dq, d["dout_q"]), (got.dk, gref.dk, d["dout_k"])):
+            want = v.to(o.dtype)
+            nan = want.isnan()
+            assert torch.equal(o.isnan(), nan)
+            assert same_bits(o.masked_fill(nan, 0)[..., keep], want.masked_fill(nan, 0)[..., keep])
+            assert same_bits(o[..., ~keep], r[..., ~keep])  # the rotated ones never see them
+
+
+@pytest.mark.parametrize("pairing", [slra.ROPE_INTERLEAVED, slra.ROPE_HALVES])
+@pytest.mark.parametrize("x", [BF, HF, FP])
+def test_rope_norm_alone_keeps_elements_apart(x, pairing):
+    """Without a rotation an infinity makes its own element NaN (inf times a reciprocal of zero) and the others of
+    its norm zero; in the gradient of the weights it stays in its own column."""
+    for norm, hq in ((slra.QK_NORM_HEAD, 2), (slra.QK_NORM_TOKEN, 2), (slra.QK_NORM_HEAD, 30), (slra.QK_NORM_TOKEN, 30)):
+        p, t, d = rope_inputs(1, 9, hq, 0, 64, x, norm=norm, rotate=False, pairing=pairing, seed=52)
+        t["q"][0, 4, 1, 7] = float("inf")
+        out, _ = slra.qk_rope_fwd(p, **t)
+        hit = out[0, 4] if norm == slra.QK_NORM_TOKEN else out[0, 4, 1:2]
+        at = 1 if norm == slra.QK_NORM_TOKEN else 0
+        assert hit[at, 7].isnan() and int(hit.isnan().sum()) == 1 and int((hit == 0).sum()) == hit.numel() - 1
+        assert int(out.isnan().sum()) == 1
+        p, t, d = rope_inputs(1, 9, hq, 0, 64, x, norm=norm, rotate=False, pairing=pairing, seed=52)
+        d["dout_q"][0, 4, 1, 7] = float("inf")
+        g = slra.qk_rope_bwd(p, t["q"], None, d["dout_q"], wq=t["wq"])
+        column = 64 + 7 if norm == slra.QK_NORM_TOKEN else 7
+        assert g.dwq[column].isinf() and int(g.dwq.isfinite().sum()) == g.dwq.numel() - 1
+
+
+@pytest.mark.parametrize("x,out", [(BF, BF), (HF, HF), (FP, FP), (BF, FP), (HF, FP)])
+@pytest.mark.parametrize("norm", [slra.QK_NORM_HEAD, slra.QK_NORM_TOKEN])
+@pytest.mark.parametrize("B,L,hq,hk,D", [(1, 1, 12, 12, 128), (2, 700, 12, 12, 128), (1, 900, 40, 40, 128), (3, 41, 24, 3, 80),
+                                         (1, 77, 5, 0, 64)])
+def test_rope_norm_alone(x, out, norm, B, L, hq, hk, D):
+    """The QK norm as the attention wants it, gradients in fp32 as its backward writes them."""
+    code = {BF: slra.DTYPE_BF16, HF: slra.DTYPE_F16, FP: slra.DTYPE_F32}[out]
+    p, t, d = rope_inputs(B, L, hq, hk, D, x, out, x, norm, rotate=False, out_dtype=code, seed=53)
+    check_rope(p, t, d)
