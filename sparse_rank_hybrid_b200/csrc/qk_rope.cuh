@@ -31,7 +31,10 @@
 
 namespace slra {
 
-constexpr size_t kRopeRingBytes = 200 * 1024;  // dynamic shared memory of an SM's blocks at most
+constexpr size_t kRopeRingBytes = 200 * 1024;  // dynamic shared memory of the rings of an SM's blocks at most
+// and of a block's tables: two steps of two tokens for each team, whose heads have 256 elements, or 1024 together
+// where teams share a block
+constexpr size_t kRopeTableBytes = 2 * 2 * 1024 * sizeof(float);
 
 // Tokens that a team takes at a time, for V vectors a thread: what a step costs besides its vectors (the
 // loop, the ring, the table, the barrier and the sums' exchanges) is shared by them, while the weights and
@@ -413,11 +416,8 @@ cudaError_t rope_launch(QkRopeArgs a, const RowPlan& p, cudaStream_t st) {
     a.stages = ring_stages(stage, per_sm, kRopeRingBytes / per_sm, a.share, R);
     const size_t smem = a.stages * stage + size_t(p.threads / p.team) * 2 * R * a.head_dim * sizeof(float);
     const auto kernel = qk_rope_kernel<TX, TO, VQ, VK, HALVES, BWD, WIDE, NORM, ALL>;
-    if (smem > 40 * 1024) {  // 48 KB without opting in, less the static part
-        const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_shared(kernel, smem, kRopeRingBytes + kRopeTableBytes);
+    if (e != cudaSuccess) return e;
     kernel<<<p.blocks, p.threads, smem, st>>>(a);
     return cudaGetLastError();
 }

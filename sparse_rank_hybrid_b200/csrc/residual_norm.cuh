@@ -803,11 +803,8 @@ inline int blocks_per_sm(const RowPlan& p, bool backward) {
 
 template <typename K>
 cudaError_t launch(K kernel, const ResidualNormArgs& a, const RowPlan& p, size_t smem, cudaStream_t st) {
-    if (smem > 40 * 1024) {  // 48 KB without opting in, less the static part
-        const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_shared(kernel, smem, kRingBytes);
+    if (e != cudaSuccess) return e;
     kernel<<<p.blocks, p.threads, smem, st>>>(a);
     return cudaGetLastError();
 }

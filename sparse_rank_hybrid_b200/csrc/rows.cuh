@@ -378,6 +378,14 @@ inline int ring_stages(size_t stage, int blocks_per_sm, size_t room, long long m
     return n;
 }
 
+// Before a launch with `bytes` of dynamic shared memory.  The limit belongs to the function, not to the call: `most`
+// is the same in every call of a kernel, or one call could lower it between another host thread's setting and launch.
+template <typename K>
+cudaError_t allow_shared(K kernel, size_t bytes, size_t most) {
+    if (bytes <= 40 * 1024) return cudaSuccess;  // 48 KB without opting in, less the static part
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+}
+
 // The sums of partial sums: kernels of `kFinalWarps` warps a block.  Where a job has many, the blocks of a
 // cluster share it.
 constexpr int kFinalWarps = 16;

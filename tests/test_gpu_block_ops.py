@@ -949,3 +949,52 @@ def test_rope_norm_alone(x, out, norm, B, L, hq, hk, D):
     code = {BF: slra.DTYPE_BF16, HF: slra.DTYPE_F16, FP: slra.DTYPE_F32}[out]
     p, t, d = rope_inputs(B, L, hq, hk, D, x, out, x, norm, rotate=False, out_dtype=code, seed=53)
     check_rope(p, t, d)
+
+
+def test_calls_from_several_host_threads_at_once():
+    """Calls of one kernel at several sizes of its shared memory, from host threads of their own: none is refused,
+    and every answer has its bits."""
+    import ctypes
+    import threading
+    L = slra.lib()
+    cases = []
+    for C in (5120, 4096, 2560):
+        p, t, d = norm_inputs(1, 1500, C, seed=C)
+        ref = slra.residual_norm_bwd(p, **t, **d)
+        f = slra.residual_norm_fwd(p, **t)
+        c = slra._residual_norm_problem(p, t["x"], t["y"], d["dh"], *(t[n] for n in ("gate", "scale", "shift", "weight", "bias",
+                                                                                     "post_weight")))[0]
+        own, ob = [torch.empty_like(v) for v in f], [torch.empty_like(v) for v in (ref.dx, ref.dy)]
+        a = [v.data_ptr() for v in (t["x"], t["y"], *own)]
+        b = [v.data_ptr() for v in (t["x"], t["y"], d["dx_out"], d["dh"], *ob)]
+        cases.append((lambda s, c=c, a=a: L.slra_residual_norm_fwd(ctypes.byref(c), *a, s), own, f, (t, c)))
+        cases.append((lambda s, c=c, b=b: L.slra_residual_norm_bwd(ctypes.byref(c), *b, None, 0, s), ob, (ref.dx, ref.dy), (d, c)))
+    for heads in (40, 32, 20):
+        p, t, d = rope_inputs(1, 1500, heads, heads, 128, grid=(5, 20, 15), seed=heads)
+        f, g = slra.qk_rope_fwd(p, **t), slra.qk_rope_bwd(p, t["q"], t["k"], **d, wq=t["wq"], wk=t["wk"])
+        c = slra._qk_rope_problem(p, t["q"], t["k"], t["wq"], t["wk"], None)[0]
+        c.out_dtype = c.x_dtype
+        own, ob = [torch.empty_like(v) for v in f], [torch.empty_like(v) for v in (g.dq, g.dk)]
+        a = [v.data_ptr() for v in (t["q"], t["k"], *own)]
+        b = [v.data_ptr() for v in (t["q"], t["k"], d["dout_q"], d["dout_k"], *ob)]
+        cases.append((lambda s, c=c, a=a: L.slra_qk_rope_fwd(ctypes.byref(c), *a, s), own, f, (t, c)))
+        cases.append((lambda s, c=c, b=b: L.slra_qk_rope_bwd(ctypes.byref(c), *b, None, 0, s), ob, (g.dq, g.dk), (d, c)))
+    torch.cuda.synchronize()
+    streams, refused = [torch.cuda.Stream() for _ in cases], [0] * len(cases)
+    start = threading.Barrier(len(cases))
+
+    def work(i):
+        call, s = cases[i][0], streams[i].cuda_stream
+        start.wait()
+        for _ in range(2000):
+            refused[i] += call(s) != slra.OK
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert refused == [0] * len(cases)
+    for _, got, ref, _ in cases:
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
