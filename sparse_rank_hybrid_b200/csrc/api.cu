@@ -30,7 +30,6 @@ __global__ void status_or_global_kernel(const int* src) {
 
 namespace {
 
-constexpr int64_t kMaxBlocks = 2048;  // selection keeps a row of scores in shared memory
 // The branch entry points size their workspace with the parameters the branch does not use set to these.
 constexpr int kSparseOnlyRank = 16;
 constexpr int kLowrankOnlyBlock = 128;

@@ -226,9 +226,9 @@ __global__ void __launch_bounds__(NTH, NTH == 256 ? 2 : 3) rope_pool_kernel(cons
 
 // The q, k (and v) tiles, or the block-sum exchange that later reuses them ([threads/(D/8)][4][D/2]
 // fp64 = threads/8 KB for any D), whichever is larger.
-size_t rope_pool_smem_bytes(const Geom& g, bool write_v, int threads) {
-    const size_t tiles = static_cast<size_t>(write_v ? 3 : 2) * g.block * g.D * 2;
-    const size_t red = static_cast<size_t>(threads / (g.D / 8)) * 4 * (g.D / 2) * 8;
+static size_t rope_pool_smem_bytes(int block, int D, bool write_v, int threads) {
+    const size_t tiles = static_cast<size_t>(write_v ? 3 : 2) * block * D * 2;
+    const size_t red = static_cast<size_t>(threads / (D / 8)) * 4 * (D / 2) * 8;
     return (tiles > red ? tiles : red) + 1024;
 }
 
@@ -240,8 +240,11 @@ static cudaError_t launch_rope_pool_t(const CUtensorMap& tm_q, const CUtensorMap
     // without v: three CTAs of 128 threads per SM (more blocks in flight); with v: two of 256
     constexpr int NTH = kV ? 256 : 128;
     dim3 grid(g.BH(), g.nb);
-    const int sm = static_cast<int>(rope_pool_smem_bytes(g, kV, NTH));
-    cudaError_t e = cudaFuncSetAttribute(rope_pool_kernel<D, kV, NTH>, cudaFuncAttributeMaxDynamicSharedMemorySize, sm);
+    const size_t sm = rope_pool_smem_bytes(g.block, D, kV, NTH);
+    // the limit belongs to the function: the same for every block size, so that no call lowers another's
+    const size_t most = rope_pool_smem_bytes(kMaxBlockTokens, D, kV, NTH);
+    cudaError_t e = cudaFuncSetAttribute(rope_pool_kernel<D, kV, NTH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(most));
     if (e != cudaSuccess) return e;
     rope_pool_kernel<D, kV, NTH><<<grid, NTH, sm, st>>>(tm_q, tm_k, tm_v, tab, pairs, g, qh, kh, vh, qbar, kbar,
                                                         status, timeout_ns);
@@ -425,21 +428,22 @@ __global__ void __launch_bounds__(256, 2) select_kernel(const double* __restrict
     }
 }
 
-static size_t select_smem(const Geom& g) {
-    return sizeof(double) * static_cast<size_t>(kSelRows) * g.nb + sizeof(int) * kSelRows * 256;
+static constexpr size_t select_smem(int nb) {
+    return sizeof(double) * static_cast<size_t>(kSelRows) * nb + sizeof(int) * kSelRows * 256;
 }
 
 cudaError_t launch_select(const double* qbar, const double* kbar, const Geom& g, int32_t* idx, uint8_t* tie,
                           cudaStream_t st) {
     dim3 grid((g.nb + kSelRows - 1) / kSelRows, g.BH());
-    const size_t sm = select_smem(g);
+    const size_t sm = select_smem(g.nb);
+    constexpr int most = static_cast<int>(select_smem(kMaxBlocks));  // the same limit for every length, as above
     cudaError_t e;
     if (g.D == 128) {
-        e = cudaFuncSetAttribute(select_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+        e = cudaFuncSetAttribute(select_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
         select_kernel<128><<<grid, 256, sm, st>>>(qbar, kbar, g, idx, tie);
     } else {
-        e = cudaFuncSetAttribute(select_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+        e = cudaFuncSetAttribute(select_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
         select_kernel<64><<<grid, 256, sm, st>>>(qbar, kbar, g, idx, tie);
     }

@@ -207,3 +207,42 @@ def test_v_copy_only_where_the_backward_reads_it(w):
     slra.attn_fwd_train(p, t["q"], t["k"], t["v"], t["A"], workspace=wst)
     assert slra.device_status(wst) == slra.OK
     assert torch.equal(slra.ws_view(p, wst, "vh"), expect)
+
+
+def test_selections_from_several_host_threads_at_once():
+    """Block selections of several shapes from host threads of their own: their kernels are shared and ask for other
+    sizes of shared memory at other blocks and lengths, and no call is refused for another's."""
+    import ctypes
+    import threading
+
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(30)
+    cases = []
+    for T, H, W, block in [(1, 8, 16, 64), (2, 8, 16, 128)] * 6 + [(30, 40, 40, 64), (60, 40, 40, 64)]:
+        prob = slra.Problem(batch=1, heads=1, head_dim=128, T=T, H=H, W=W, block=block, keep_frac=0.5, rank=32)
+        q, k, v = (torch.randn((1, T * H * W, 1, 128), generator=g, device="cuda").bfloat16() for _ in range(3))
+        ws = slra.select_blocks(prob, q, k, v)
+        own = torch.empty_like(ws)
+        cases.append((prob, prob.c(), [x.data_ptr() for x in (q, k, v, own)], own, ws, (q, k, v)))
+    torch.cuda.synchronize()
+    streams, refused = [torch.cuda.Stream() for _ in cases], [0] * len(cases)
+    start = threading.Barrier(len(cases))
+
+    def work(i):
+        _, c, a, own, _, _ = cases[i]
+        s, n, call = streams[i].cuda_stream, own.numel(), slra.lib().slra_select_blocks
+        start.wait()
+        for _ in range(1500):
+            refused[i] += call(ctypes.byref(c), *a, n, s) != slra.OK
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert refused == [0] * len(cases)
+    for prob, _, _, own, ws, _ in cases:
+        assert slra.device_status(own) == slra.OK
+        for n in ("qh", "kh", "idx"):
+            assert torch.equal(slra.ws_view(prob, own, n), slra.ws_view(prob, ws, n))
