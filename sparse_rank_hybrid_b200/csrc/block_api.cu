@@ -14,38 +14,86 @@ bool known_dtype(int32_t d) { return d == SLRA_DTYPE_BF16 || d == SLRA_DTYPE_F32
 int64_t size_of(int32_t dtype) { return dtype == SLRA_DTYPE_F32 ? 4 : 2; }
 bool positive(float x) { return x > 0.f && std::isfinite(x); }
 
-// What a tensor of rows covers: `width` bytes of every token.
+// What a tensor covers: pieces of `run` bytes, n[i] of them at a stride of s[i] bytes in each of its dimensions
+// (batch, token, head).
 struct Region {
     uintptr_t at;
-    int64_t extent, width, period;  // bytes; period: distance of neighbouring rows, 0 = one piece
-    int64_t sb, sl;                 // strides (bytes), to tell an exact alias
+    int64_t run, extent, n[3], s[3];
 };
 
 Region region(const void* p, int64_t elem, const Strides& st, int64_t B, int64_t L, int64_t Hh, int64_t D) {
-    Region r;
-    r.at = reinterpret_cast<uintptr_t>(p);
-    r.extent = extent_elems(st, B, L, Hh, D) * elem;
-    r.width = ((Hh - 1) * st.h + D) * elem;
-    r.sb = st.b * elem;
-    r.sl = st.l * elem;
-    r.period = L > 1 ? (B == 1 || st.b % st.l == 0 ? r.sl : 0) : B > 1 ? r.sb : 0;
-    return r;
+    return {reinterpret_cast<uintptr_t>(p), D * elem, extent_elems(st, B, L, Hh, D) * elem, {B, L, Hh},
+            {st.b * elem, st.l * elem, st.h * elem}};
 }
-Region piece(const void* p, int64_t bytes) { return {reinterpret_cast<uintptr_t>(p), bytes, bytes, 0, 0, 0}; }
+Region piece(const void* p, int64_t bytes) { return {reinterpret_cast<uintptr_t>(p), bytes, bytes, {1, 1, 1}, {0, 0, 0}}; }
 
-// Whether two regions may share a byte.  Rows of one period that interleave (views of one fused buffer)
-// do not.
-bool conflict(const Region& a, const Region& b) {
+// The strides of two regions, the largest first, with each one's number of steps and what it spans from there on
+// inwards.
+struct Meeting {
+    int levels, left;  // left: places that may still be looked at
+    int64_t s[6], na[6], nb[6], span_a[7], span_b[7];
+
+    Meeting(const Region& a, const Region& b) : levels(0), left(256) {
+        for (const Region* r : {&a, &b})
+            for (int i = 0; i < 3; ++i) {
+                if (r->n[i] == 1) continue;
+                int at = 0;
+                while (at < levels && s[at] > r->s[i]) ++at;
+                if (at == levels || s[at] != r->s[i]) {
+                    for (int j = levels++; j > at; --j) s[j] = s[j - 1], na[j] = na[j - 1], nb[j] = nb[j - 1];
+                    s[at] = r->s[i];
+                    na[at] = nb[at] = 1;
+                }
+                (r == &a ? na : nb)[at] += r->n[i] - 1;
+            }
+        span_a[levels] = a.run;
+        span_b[levels] = b.run;
+        for (int i = levels - 1; i >= 0; --i) {
+            span_a[i] = span_a[i + 1] + (na[i] - 1) * s[i];
+            span_b[i] = span_b[i + 1] + (nb[i] - 1) * s[i];
+        }
+    }
+    // Whether any of the pieces meet, from level i inwards, where b's first lies d behind a's: b's step minus a's
+    // takes each value k of a range, and only those that bring the spans together are followed.
+    bool meet(int i, int64_t d) {
+        if (d >= span_a[i] || -d >= span_b[i]) return false;
+        if (i == levels) return true;
+        const auto floor_div = [](int64_t x, int64_t y) { return x / y - (x % y < 0); };
+        const int64_t lo = std::max(-floor_div(span_b[i + 1] - 1 + d, s[i]), 1 - na[i]);
+        const int64_t hi = std::min(floor_div(span_a[i + 1] - 1 - d, s[i]), nb[i] - 1);
+        for (int64_t k = lo; k <= hi; ++k) {
+            if (--left < 0) return true;  // strides that do not nest: taken as a conflict
+            if (meet(i + 1, d + k * s[i])) return true;
+        }
+        return false;
+    }
+};
+
+// Whether tokens of one stride leave room for each other, as those of a fused buffer [q | k | v] do: most views
+// that meet in their extents, at a fraction of what following the strides takes.
+bool tokens_interleave(const Region& a, const Region& b) {
+    const int64_t s = a.s[1];
+    if (a.n[1] == 1 || b.n[1] == 1 || b.s[1] != s || (a.n[0] > 1 && a.s[0] % s != 0) || (b.n[0] > 1 && b.s[0] % s != 0))
+        return false;
+    int64_t d = static_cast<int64_t>(b.at - a.at) % s;
+    if (d < 0) d += s;
+    return d >= (a.n[2] - 1) * a.s[2] + a.run && d + (b.n[2] - 1) * b.s[2] + b.run <= s;
+}
+
+bool pieces_meet(const Region& a, const Region& b) {
+    return !tokens_interleave(a, b) && Meeting(a, b).meet(0, static_cast<int64_t>(b.at - a.at));
+}
+
+// Whether two regions may share a byte.  Views of one buffer whose rows, heads or samples interleave do not.
+inline bool conflict(const Region& a, const Region& b) {
     if (!a.at || !b.at) return false;
     const uintptr_t ae = a.at + static_cast<uintptr_t>(a.extent), be = b.at + static_cast<uintptr_t>(b.extent);
-    if (a.at >= be || b.at >= ae) return false;
-    if (a.period == 0 || a.period != b.period) return true;
-    int64_t d = static_cast<int64_t>(b.at - a.at) % a.period;
-    if (d < 0) d += a.period;
-    return !(d >= a.width && d + b.width <= a.period);
+    return a.at < be && b.at < ae && pieces_meet(a, b);
 }
 bool same(const Region& a, const Region& b) {
-    return a.at == b.at && a.extent == b.extent && a.width == b.width && a.sb == b.sb && a.sl == b.sl;
+    for (int i = 0; i < 3; ++i)
+        if (a.n[i] != b.n[i] || (a.n[i] > 1 && a.s[i] != b.s[i])) return false;
+    return a.at == b.at && a.run == b.run;
 }
 
 // Runs body(workspace) on the caller's workspace, or on one allocated and freed on `st` where that is NULL.
@@ -359,8 +407,8 @@ slra_status slra_residual_norm_fwd(const slra_residual_norm* p, const void* x, c
     const Region ro = rows_region(p, x_out, p->stream_dtype, d.x_out), rh = rows_region(p, h, p->block_dtype, d.h);
     Region vec[12];
     vector_regions(p, d, vec);
-    if ((conflict(ro, rx) && !same(ro, rx)) || conflict(ro, ry) || conflict(ro, rh) || conflict(rh, rx) ||
-        (conflict(rh, ry) && !same(rh, ry)))
+    if ((!same(ro, rx) && conflict(ro, rx)) || conflict(ro, ry) || conflict(ro, rh) || conflict(rh, rx) ||
+        (!same(rh, ry) && conflict(rh, ry)))
         return SLRA_ERR_INVALID_ARG;
     for (int i = 0; i < 6; ++i)
         if (conflict(ro, vec[i]) || conflict(rh, vec[i])) return SLRA_ERR_INVALID_ARG;
@@ -396,9 +444,9 @@ slra_status slra_residual_norm_bwd(const slra_residual_norm* p, const void* x, c
     const Region ws = piece(workspace, static_cast<int64_t>(workspace_bytes));
     Region vec[12];
     vector_regions(p, d, vec);
-    if (conflict(rdx, in[0]) || conflict(rdx, in[1]) || (conflict(rdx, in[2]) && !same(rdx, in[2])) ||
+    if (conflict(rdx, in[0]) || conflict(rdx, in[1]) || (!same(rdx, in[2]) && conflict(rdx, in[2])) ||
         conflict(rdx, in[3]) || conflict(rdy, in[0]) || conflict(rdy, in[1]) || conflict(rdy, in[2]) ||
-        (conflict(rdy, in[3]) && !same(rdy, in[3])) || conflict(rdx, rdy) || conflict(rdx, ws) || conflict(rdy, ws))
+        (!same(rdy, in[3]) && conflict(rdy, in[3])) || conflict(rdx, rdy) || conflict(rdx, ws) || conflict(rdy, ws))
         return SLRA_ERR_INVALID_ARG;
     for (int i = 0; i < 12; ++i) {
         if (conflict(rdx, vec[i]) || conflict(rdy, vec[i]) || conflict(ws, vec[i])) return SLRA_ERR_INVALID_ARG;
@@ -470,10 +518,10 @@ slra_status slra_qk_rope_fwd(const slra_qk_rope* p, const void* q, const void* k
     const Region rq = heads_region(p, q, p->x_dtype, d.q, p->heads), rk = heads_region(p, k, p->x_dtype, d.k, p->kv_heads);
     const Region oq = heads_region(p, out_q, p->out_dtype, d.out_q, p->heads);
     const Region ok = heads_region(p, out_k, p->out_dtype, d.out_k, p->kv_heads);
-    const bool q_in_place = same(oq, rq) && d.q.h == d.out_q.h && p->x_dtype == p->out_dtype;
-    const bool k_in_place = same(ok, rk) && d.k.h == d.out_k.h && p->x_dtype == p->out_dtype;
-    if ((conflict(oq, rq) && !q_in_place) || conflict(oq, rk) || conflict(oq, ok) || conflict(ok, rq) ||
-        (conflict(ok, rk) && !k_in_place))
+    const bool q_in_place = same(oq, rq) && p->x_dtype == p->out_dtype;
+    const bool k_in_place = same(ok, rk) && p->x_dtype == p->out_dtype;
+    if ((!q_in_place && conflict(oq, rq)) || conflict(oq, rk) || conflict(oq, ok) || conflict(ok, rq) ||
+        (!k_in_place && conflict(ok, rk)))
         return SLRA_ERR_INVALID_ARG;
     const int64_t W = size_of(p->weight_dtype);
     for (const Region& r : {positions_region(p), weight_region(p, p->wq, p->heads, W), weight_region(p, p->wk, p->kv_heads, W)})
@@ -515,10 +563,10 @@ slra_status slra_qk_rope_bwd(const slra_qk_rope* p, const void* q, const void* k
     const Region rdk = heads_region(p, dk, p->x_dtype, d.dk, p->kv_heads);
     const Region rgq = heads_region(p, dout_q, p->out_dtype, d.out_q, p->heads);
     const Region rgk = heads_region(p, dout_k, p->out_dtype, d.out_k, p->kv_heads);
-    const bool q_in_place = same(rdq, rgq) && d.dq.h == d.out_q.h && p->x_dtype == p->out_dtype;
-    const bool k_in_place = same(rdk, rgk) && d.dk.h == d.out_k.h && p->x_dtype == p->out_dtype;
-    if ((conflict(rdq, rgq) && !q_in_place) || conflict(rdq, rgk) || conflict(rdq, rdk) || conflict(rdk, rgq) ||
-        (conflict(rdk, rgk) && !k_in_place))
+    const bool q_in_place = same(rdq, rgq) && p->x_dtype == p->out_dtype;
+    const bool k_in_place = same(rdk, rgk) && p->x_dtype == p->out_dtype;
+    if ((!q_in_place && conflict(rdq, rgq)) || conflict(rdq, rgk) || conflict(rdq, rdk) || conflict(rdk, rgq) ||
+        (!k_in_place && conflict(rdk, rgk)))
         return SLRA_ERR_INVALID_ARG;
     const int64_t W = size_of(p->weight_dtype);
     const Region ws = piece(workspace, static_cast<int64_t>(workspace_bytes));

@@ -195,6 +195,62 @@ def test_rope_argument_validation():
     assert rope_bwd(h, ws=at(0)) == INV and rope_bwd(rope_problem(positions=at(4) + 64, W=1)) == INV
 
 
+def test_views_of_one_buffer_over_a_batch():
+    """Slices of one buffer whose samples interleave do not meet; a row further they do."""
+    INV, DEV = slra.ERR_INVALID_ARG, slra.ERR_NO_DEVICE
+    B, L, H, D = 2, 24, 4, 64
+    one = L * H * D  # elements of a sample's slice
+    for token, head in ((H * D, D), (D, L * D)):  # [B, 3, L, H, D] and [B, 3, H, L, D]
+        st = (3 * one, token, head)
+        f = dict(kv_heads=4, **{n + "_strides": st for n in ("q", "k", "out_q", "out_k", "dq", "dk")})
+        q, k, v = at(0), at(0) + 2 * one, at(0) + 4 * one
+        assert rope_fwd(rope_problem(**f), q, k, q, k) == DEV and rope_fwd(rope_problem(**f), q, k, v, at(1)) == DEV
+        assert rope_fwd(rope_problem(**f), q, k, q, k - 2 * D) == INV and rope_fwd(rope_problem(**f), q, k, at(1), v + 2 * D) == INV
+        n = dict(f, norm=HEAD)
+        assert rope_bwd(rope_problem(**n), at(0), at(0) + 2 * one, at(1), at(1) + 2 * one, at(2), at(2) + 2 * one) == DEV
+        assert rope_bwd(rope_problem(**n), at(0), at(0) + 2 * one, at(1), at(1) + 2 * one, at(2), at(2) + 2 * one - 16) == INV
+    one = 24 * 64
+    s = {n + "_strides": (4 * one, 64) for n in ("x", "y", "x_out", "h")}
+    slices = [at(0) + 2 * one * i for i in range(4)]
+    assert norm_fwd(norm_problem(**s), *slices) == DEV and norm_fwd(norm_problem(**s), *slices[::-1]) == DEV
+    assert norm_fwd(norm_problem(**s), *slices[:3], slices[3] + 16) == INV
+    # a stride that a single sample never takes is nothing to compare
+    assert norm_fwd(norm_problem(batch=1, x_strides=(8, 64)), x_out=at(0)) == DEV
+
+
+def test_regions_against_every_piece():
+    """The check of overlaps against the sets of pieces: never passes an overlap, and refuses views of the same
+    strides only for one."""
+    import random
+    rng = random.Random(1)
+    INV, DEV = slra.ERR_INVALID_ARG, slra.ERR_NO_DEVICE
+    counts = {INV: 0, DEV: 0}
+    for _ in range(4000):
+        B, L, H = rng.randint(1, 3), rng.randint(1, 4), rng.randint(1, 4)
+        def strides():
+            dims, span, st = [(0, B), (1, L), (2, H)], 8, [8, 8, 8]
+            rng.shuffle(dims)
+            for i, n in dims:
+                st[i] = span + 8 * rng.choice([0, 0, 0, 1, 2, 5, 12])
+                span += st[i] * (n - 1)
+            return tuple(st)
+        a = strides()
+        b = a if rng.random() < 0.7 else strides()
+        d = 8 * rng.randint(-30, 30)
+        def pieces(st, off):
+            return {off + i * st[0] + j * st[1] + k * st[2] for i in range(B) for j in range(L) for k in range(H)}
+        meet = bool(pieces(a, 0) & pieces(b, d))
+        c = rope_problem(batch=B, tokens=L, W=L, heads=H, kv_heads=0, head_dim=8, q_strides=a, out_q_strides=b)
+        got = rope_fwd(c, at(1), None, at(1) + 2 * d, None)
+        in_place = d == 0 and all(x == y or n == 1 for x, y, n in zip(a, b, (B, L, H)))
+        counts[got] += 1
+        if meet and not in_place:
+            assert got == INV, (B, L, H, a, b, d)
+        elif a == b or in_place:
+            assert got == DEV, (B, L, H, a, b, d)
+    assert min(counts.values()) > 500
+
+
 def test_workspaces_hold_a_bounded_number_of_partial_sums():
     """The partial sums grow with the workers, which are bounded, not with the tokens."""
     L = slra.lib()

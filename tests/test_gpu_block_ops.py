@@ -998,3 +998,46 @@ def test_calls_from_several_host_threads_at_once():
     assert refused == [0] * len(cases)
     for _, got, ref, _ in cases:
         assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+@pytest.mark.parametrize("order", ["token", "head"])
+def test_rope_slices_of_one_buffer_over_a_batch(order):
+    """q and k as slices of one [B, 3, ...] tensor, rotated in place, and gradients into slices of one: the samples of
+    the slices interleave, their elements do not meet."""
+    B, L, H, D = 3, 23, 4, 64
+    p, t, d = rope_inputs(B, L, H, H, D, norm=slra.QK_NORM_HEAD, grid=(2, 4, 3), seed=54)
+    ref, bwd = slra.qk_rope_fwd(p, **t), slra.qk_rope_bwd(p, t["q"], t["k"], **d, wq=t["wq"], wk=t["wk"])
+
+    def slices(fill):
+        if order == "token":
+            buf = torch.full((B, 3, L, H, D), fill, dtype=BF, device="cuda")
+            return buf, [buf[:, i] for i in range(3)]
+        buf = torch.full((B, 3, H, L, D), fill, dtype=BF, device="cuda")
+        return buf, [buf[:, i].transpose(1, 2) for i in range(3)]
+
+    _, (q, k, v) = slices(3.0)
+    q.copy_(t["q"]), k.copy_(t["k"])
+    _, (dq, dk, dv) = slices(5.0)
+    slra.qk_rope_bwd(p, q, k, **d, wq=t["wq"], wk=t["wk"], dq=dq, dk=dk)
+    assert torch.equal(dq, bwd.dq) and torch.equal(dk, bwd.dk) and (dv == 5).all()
+    slra.qk_rope_fwd(p, q, k, t["wq"], t["wk"], out_q=q, out_k=k)
+    assert torch.equal(q, ref[0]) and torch.equal(k, ref[1]) and (v == 3).all()
+
+
+def test_norm_slices_of_one_buffer_over_a_batch():
+    """x, y, x_out and h as slices of one [B, 4, L, C] tensor, gradients into slices of one."""
+    B, L, C = 3, 29, 320
+    p, t, d = norm_inputs(B, L, C, seed=55)
+    ref, bwd = slra.residual_norm_fwd(p, **t), slra.residual_norm_bwd(p, **t, **d)
+    buf = torch.full((B, 4, L, C), 3.0, dtype=BF, device="cuda")
+    x, y, x_out, h = (buf[:, i] for i in range(4))
+    x.copy_(t["x"]), y.copy_(t["y"])
+    s = dict(t, x=x, y=y)
+    slra.residual_norm_fwd(p, **s, x_out=x_out, h=h)
+    assert torch.equal(x_out, ref[0]) and torch.equal(h, ref[1]) and torch.equal(x, t["x"]) and torch.equal(y, t["y"])
+    x_out.copy_(d["dx_out"]), h.copy_(d["dh"])
+    out = torch.full((B, 3, L, C), 5.0, dtype=BF, device="cuda")
+    slra.residual_norm_bwd(p, **s, dx_out=x_out, dh=h, dx=out[:, 2], dy=out[:, 0])
+    assert torch.equal(out[:, 2], bwd.dx) and torch.equal(out[:, 0], bwd.dy) and (out[:, 1] == 5).all()
+    slra.residual_norm_bwd(p, **s, dx_out=x_out, dh=h, dx=x_out, dy=h)
+    assert torch.equal(x_out, bwd.dx) and torch.equal(h, bwd.dy)
