@@ -629,7 +629,9 @@ typedef enum slra_rope_schedule { SLRA_ROPE_PER_AXIS = 0, SLRA_ROPE_SHARED = 1 }
  *                            only where the weight itself is given.
  *   *_strides                element strides (batch, token, head), all zero (default) = contiguous, else
  *                            positive multiples of 16 bytes below 2^36 (e.g. views of a fused QKV
- *                            buffer); a backward's dout_q, dout_k use out_q_strides, out_k_strides.
+ *                            buffer), a token's heads within 2^31 elements ((heads - 1) * the head
+ *                            stride + head_dim); a backward's dout_q, dout_k use out_q_strides,
+ *                            out_k_strides.
  */
 typedef struct slra_qk_rope {
     int64_t batch, tokens, heads, kv_heads, head_dim;

@@ -294,8 +294,11 @@ slra_status derive(const slra_qk_rope* p, Heads* d) {
         !strides_of(p->out_q_strides, L, hq, D, O, &d->out_q) || !strides_of(p->out_k_strides, L, hk, D, O, &d->out_k) ||
         !strides_of(p->dq_strides, L, hq, D, X, &d->dq) || !strides_of(p->dk_strides, L, hk, D, X, &d->dk))
         return SLRA_ERR_INVALID_ARG;
-    for (const Strides* st : {&d->q, &d->k, &d->out_q, &d->out_k, &d->dq, &d->dk})  // 32-bit places in a token
-        if ((std::max(hq, hk) - 1) * st->h + D >= most) return SLRA_ERR_UNSUPPORTED;
+    // a token's heads within 2^31 elements
+    for (const Strides* st : {&d->q, &d->out_q, &d->dq})
+        if ((hq - 1) * st->h + D >= most) return SLRA_ERR_UNSUPPORTED;
+    for (const Strides* st : {&d->k, &d->out_k, &d->dk})
+        if ((hk - 1) * st->h + D >= most) return SLRA_ERR_UNSUPPORTED;
 
     QkRopeArgs& a = d->a;
     std::memset(&a, 0, sizeof a);

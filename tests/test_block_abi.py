@@ -251,6 +251,18 @@ def test_regions_against_every_piece():
     assert min(counts.values()) > 500
 
 
+def test_head_strides_count_each_side():
+    """A head-major cache of 2^20 tokens: the limit on a token's reach is that of the tensor's own heads."""
+    far = 1 << 26  # 2^20 tokens of 64 elements
+    k = dict(heads=64, kv_heads=8, k_strides=(far * 8, 64, far), out_k_strides=(far * 8, 64, far), dk_strides=(far * 8, 64, far))
+    c = rope_problem(**k)
+    assert rope_fwd(c, k=at(0) + (1 << 36), ok=at(0) + (1 << 37)) == slra.ERR_NO_DEVICE
+    assert rope_bwd(c, k=at(0) + (1 << 36), gk=at(0) + (1 << 37), dk=at(0) + (1 << 38)) == slra.ERR_NO_DEVICE
+    assert rope_fwd(rope_problem(**dict(k, kv_heads=33)), k=at(0) + (1 << 36), ok=at(0) + (1 << 37)) == slra.ERR_UNSUPPORTED
+    q = dict(kv_heads=64, heads=8, q_strides=(far * 8, 64, far), out_q_strides=(far * 8, 64, far))
+    assert rope_fwd(rope_problem(**q), q=at(0) + (1 << 36), oq=at(0) + (1 << 37)) == slra.ERR_NO_DEVICE
+
+
 def test_workspaces_hold_a_bounded_number_of_partial_sums():
     """The partial sums grow with the workers, which are bounded, not with the tokens."""
     L = slra.lib()
