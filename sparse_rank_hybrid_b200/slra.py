@@ -729,10 +729,14 @@ def residual_norm_fwd(prob: ResidualNorm, x, y=None, gate=None, scale=None, shif
     """x_out = residual_scale x + gate post(y) and h = norm(x_out) (1 + scale) + shift in one pass
     (slra_residual_norm_fwd).  x: the residual stream, bf16, fp16 or fp32 [batch, tokens, channels]; y: the
     block's output (None: the norm before the first block); gate, scale, shift: [batch, groups, channels]
-    (expanded views broadcast); weight, bias, post_weight: [channels].  h gets y's type, or h_dtype (a
-    torch dtype; for a call without y, default x's).  Rows may be strided, x_out may be x and h may be y.
+    (expanded views broadcast); weight, bias, post_weight: [channels].  h has y's type; without y
+    it gets h_dtype (a torch dtype, default x's).  Rows may be strided, x_out may be x and h may be y.
     Returns (x_out, h): x itself where there is no y, None for h with NORM_NONE."""
     row, device = prob[:3], x.device
+    if h_dtype is not None:
+        block = y if y is not None else h
+        if h_dtype not in _codes() or (block is not None and block.dtype is not h_dtype):
+            raise ValueError(f"h_dtype: expected {'bf16, fp16 or fp32' if block is None else block.dtype}, got {h_dtype}")
     other = _elsewhere(x, stream)
     if other is not None:
         with other:

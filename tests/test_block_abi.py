@@ -307,3 +307,15 @@ def test_binding_strides(t, strides):
     else:
         assert slra._rows(c, "x", x, shape, torch.float32, x.device, "x_strides") == x.data_ptr()
         assert tuple(c.x_strides) == strides
+
+
+def test_binding_refuses_another_type_of_h():
+    """h has y's type: another one was given y's without a word."""
+    import torch
+    p, x, y = slra.ResidualNorm(1, 4, 64), torch.zeros((1, 4, 64)), torch.zeros((1, 4, 64), dtype=torch.bfloat16)
+    for kw in (dict(y=y, h_dtype=torch.float32), dict(h=y, h_dtype=torch.float32), dict(h_dtype=torch.float64),
+               dict(y=y, h=y, h_dtype=torch.float16)):
+        with pytest.raises(ValueError, match="h_dtype"):
+            slra.residual_norm_fwd(p, x, **kw)
+    with pytest.raises(ValueError, match="CUDA"):  # the type itself is right
+        slra.residual_norm_fwd(p, x, y=y, h_dtype=torch.bfloat16)
