@@ -815,7 +815,7 @@ class QkRope(NamedTuple):
     heads: int
     head_dim: int
     kv_heads: int = 0                # 0: no k
-    grid: tuple = None               # (T, H, W) of the positions; None: (1, 1, tokens)
+    grid: tuple = None               # (T, H, W) of the positions (tuples or lists); None: (1, 1, tokens)
     first_token: int = 0             # the grid place of token 0
     pos_offset: tuple = (0, 0, 0)
     rope_split: tuple = (0, 0, 0)    # pairs per axis; all 0: the default split
@@ -852,7 +852,12 @@ def _qk_rope_template(prob: QkRope):
 
 def _qk_rope_problem(prob, q, k, wq, wk, positions):
     """The struct filled from the inputs, and the addresses of q and k."""
-    c = _QkRope.from_buffer_copy(_qk_rope_template(prob))
+    try:
+        template = _qk_rope_template(prob)
+    except TypeError:  # lists for tuples: the templates are kept by the problem
+        template = _qk_rope_template(prob._replace(**{n: tuple(getattr(prob, n)) for n in ("grid", "pos_offset", "rope_split")
+                                                      if getattr(prob, n) is not None}))
+    c = _QkRope.from_buffer_copy(template)
     device = q.device
     batch, tokens, heads, D, kv_heads = prob[:5]
     if (k is not None) != (kv_heads > 0):

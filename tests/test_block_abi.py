@@ -319,3 +319,13 @@ def test_binding_refuses_another_type_of_h():
             slra.residual_norm_fwd(p, x, **kw)
     with pytest.raises(ValueError, match="CUDA"):  # the type itself is right
         slra.residual_norm_fwd(p, x, y=y, h_dtype=torch.bfloat16)
+
+
+def test_binding_takes_lists_for_tuples():
+    """A problem with lists gives the struct of one with tuples."""
+    import torch
+    q = torch.zeros((1, 24, 2, 64))
+    kw = dict(grid=[2, 3, 4], pos_offset=[1, 2, 3], rope_split=[8, 8, 8])
+    one = slra._qk_rope_problem(slra.QkRope(1, 24, 2, 64, **kw), q, None, None, None, None)[0]
+    two = slra._qk_rope_problem(slra.QkRope(1, 24, 2, 64, **{n: tuple(v) for n, v in kw.items()}), q, None, None, None, None)[0]
+    assert bytes(one) == bytes(two) and (one.T, one.H, one.W) == (2, 3, 4)
