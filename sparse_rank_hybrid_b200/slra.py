@@ -888,14 +888,15 @@ def qk_rope_fwd(prob: QkRope, q, k=None, wq=None, wk=None, positions=None, out_q
     contiguous last dimension, e.g. views of a fused QKV tensor); wq, wk: the norm's weights ([head_dim], or
     [heads * head_dim] with QK_NORM_TOKEN); positions: int32 [1 or batch, tokens, 3] in place of the grid.
     out_q may be q and out_k may be k.  Returns (out_q, out_k); out_k is None without k."""
-    device = q.device
+    device, code = q.device, prob.out_dtype
+    if code is not None and code not in _types():
+        raise ValueError(f"out_dtype: expected DTYPE_BF16, DTYPE_F32 or DTYPE_F16, got {code}")
     other = _elsewhere(q, stream)
     if other is not None:
         with other:
             return qk_rope_fwd(prob, q, k, wq, wk, positions, out_q, out_k)
     handle = _current_stream()(q.device.index)
     c, pq, pk = _qk_rope_problem(prob, q, k, wq, wk, positions)
-    code = prob.out_dtype
     dtype = q.dtype if code is None else _types()[code]
     c.out_dtype = c.x_dtype if code is None else code
     shape, po_k = (prob.batch, prob.tokens, prob.heads, prob.head_dim), None

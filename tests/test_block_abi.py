@@ -329,3 +329,11 @@ def test_binding_takes_lists_for_tuples():
     one = slra._qk_rope_problem(slra.QkRope(1, 24, 2, 64, **kw), q, None, None, None, None)[0]
     two = slra._qk_rope_problem(slra.QkRope(1, 24, 2, 64, **{n: tuple(v) for n, v in kw.items()}), q, None, None, None, None)[0]
     assert bytes(one) == bytes(two) and (one.T, one.H, one.W) == (2, 3, 4)
+
+
+def test_binding_refuses_an_unknown_type_of_outputs():
+    import torch
+    q = torch.zeros((1, 24, 2, 64))
+    for code in (7, torch.float32):
+        with pytest.raises(ValueError, match="out_dtype"):
+            slra.qk_rope_fwd(slra.QkRope(1, 24, 2, 64, out_dtype=code), q)
