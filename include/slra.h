@@ -253,7 +253,11 @@ typedef struct slra_ws_layout {
     size_t status, rope_table, qh, kh, vh, qbar, kbar, idx, tie, s_part, z_part, S, z;
 } slra_ws_layout;
 
-/* ABI version (SLRA_ABI_VERSION).  Never fails. */
+/*
+ * ABI version (SLRA_ABI_VERSION).  Never fails.  Functions and types that are only added leave 8 as it is:
+ * a program that may load an older library looks up what it needs (slra_residual_norm_* and slra_qk_rope_*
+ * came within 8).
+ */
 SLRA_API int slra_abi_version(void);
 
 /* Static, human-readable name of a status code.  Never returns NULL. */

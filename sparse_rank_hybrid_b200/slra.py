@@ -116,6 +116,10 @@ def lib():
         L.slra_abi_version.restype = ctypes.c_int
         if L.slra_abi_version() != ABI_VERSION:  # the structs below mirror this version of include/slra.h
             raise RuntimeError(f"{LIB_PATH} has ABI {L.slra_abi_version()}, this binding expects {ABI_VERSION}")
+        missing = [name for name in EXPORTS if not hasattr(L, name)]
+        if missing:  # functions were added without a change to what there was
+            raise RuntimeError(f"{LIB_PATH} is older than this binding (no {', '.join(missing)}): build it again with "
+                               "`python -m sparse_rank_hybrid_b200.build`")
         P, S = ctypes.c_void_p, ctypes.c_size_t
         PP = ctypes.POINTER(_Problem)
         L.slra_abi_version.restype = ctypes.c_int

@@ -337,3 +337,16 @@ def test_binding_refuses_an_unknown_type_of_outputs():
     for code in (7, torch.float32):
         with pytest.raises(ValueError, match="out_dtype"):
             slra.qk_rope_fwd(slra.QkRope(1, 24, 2, 64, out_dtype=code), q)
+
+
+def test_binding_names_what_an_older_library_lacks(tmp_path, monkeypatch):
+    """A library of the same ABI number from before functions were added."""
+    import subprocess
+    older = [n for n in slra.EXPORTS if not n.startswith(("slra_residual_norm", "slra_qk_rope"))]
+    src, so = tmp_path / "older.c", tmp_path / "older.so"
+    src.write_text("".join(f"int {n}(void) {{ return {slra.ABI_VERSION}; }}\n" for n in older))
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(so), str(src)], check=True)
+    monkeypatch.setattr(slra, "_lib", None)
+    monkeypatch.setattr(slra, "LIB_PATH", str(so))
+    with pytest.raises(RuntimeError, match="older than this binding.*slra_qk_rope_fwd"):
+        slra.lib()
