@@ -98,7 +98,7 @@ bool same(const Region& a, const Region& b) {
 
 // Runs body(workspace) on the caller's workspace, or on one allocated and freed on `st` where that is NULL.
 template <class Body>
-slra_status with_sums(size_t need, void* workspace, size_t bytes, cudaStream_t st, Body&& body) {
+slra_status with_sums(size_t need, void* workspace, cudaStream_t st, Body&& body) {
     if (workspace) return body(workspace);
     void* raw = nullptr;
     if (cudaMallocAsync(&raw, need, st) != cudaSuccess) {
@@ -478,7 +478,7 @@ slra_status slra_residual_norm_bwd(const slra_residual_norm* p, const void* x, c
     const bool mods = p->dgate || p->dscale || p->dshift, weights = p->dweight || p->dbias || p->dpost_weight;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (!mods && !weights) return cuda_status(launch_residual_norm(a, true, st));
-    return with_sums(d.bytes, workspace, workspace_bytes, st, [&](void* ws_ptr) {
+    return with_sums(d.bytes, workspace, st, [&](void* ws_ptr) {
         uint8_t* base = static_cast<uint8_t*>(ws_ptr);
         a.part = mods ? reinterpret_cast<float*>(base + d.part) : nullptr;
         a.wpart = weights ? reinterpret_cast<float*>(base + d.wpart) : nullptr;
@@ -608,7 +608,7 @@ slra_status slra_qk_rope_bwd(const slra_qk_rope* p, const void* q, const void* k
     a.side[1].dweight = p->dwk;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (!p->dwq && !p->dwk) return cuda_status(launch_qk_rope(a, true, st));
-    return with_sums(d.bytes, workspace, workspace_bytes, st, [&](void* ws_ptr) {
+    return with_sums(d.bytes, workspace, st, [&](void* ws_ptr) {
         a.part = static_cast<float*>(ws_ptr);
         return cuda_status(launch_qk_rope(a, true, st));
     });

@@ -129,6 +129,7 @@ __device__ __forceinline__ void each_row(const Place<WIDE>& at, Row row) {
 
 // The sum over a block's teams (each `size` lanes of its four warps) of a thread's four values, in a fixed
 // order, in the threads of the first team.
+constexpr int kJoinScratch = 4 * 128;  // floats of shared memory
 __device__ __forceinline__ float4 join_teams(float4 u, int size, float* scratch) {
     for (int o = size; o < 32; o *= 2) {
         u.x += __shfl_xor_sync(0xffffffffu, u.x, o), u.y += __shfl_xor_sync(0xffffffffu, u.y, o);
@@ -413,7 +414,7 @@ __global__ void __launch_bounds__(WIDE ? bwd_threads(V, Y == 2 && !TOKEN) : 128,
     // x, dx_out, dh and y of each vector
     constexpr int DXO = UX, DH = 2 * UX, YU = 2 * UX + UB, ONE = 2 * UX + (Y ? 2 : 1) * UB, U = V * ONE;
     extern __shared__ uint4 shared[];
-    __shared__ __align__(16) float scratch[kTeamScratch];
+    __shared__ __align__(16) float scratch[WIDE ? kTeamScratch : kJoinScratch];
     const Place<WIDE> at(a);
     Team<WIDE> team(at.size, scratch);
     const int c0 = at.t * (SPLIT ? 4 : 8), step = at.size * (SPLIT ? 4 : 8), gap = SPLIT ? a.channels / 2 : 4;

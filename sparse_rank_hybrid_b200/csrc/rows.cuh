@@ -252,7 +252,8 @@ struct Feed {
 
 // A team of threads shares a row: the whole block (WIDE; a multiple of 32 threads, at most 1024), or
 // `size` threads of a warp, a power of two (then several teams in a block).
-constexpr int kTeamScratch = 2 * 8 * 32;  // floats of shared memory for a block-wide team's sums
+constexpr int kTeamSums = 4;                      // values that are summed at once, at most
+constexpr int kTeamScratch = 2 * kTeamSums * 32;  // floats of shared memory for a block-wide team's sums
 
 template <bool WIDE>
 struct Team {
@@ -273,13 +274,13 @@ struct Team {
     static __device__ __forceinline__ float swap(float x, int o) { return __shfl_xor_sync(0xffffffffu, x, o); }
 
     // Every value summed over the team, in a fixed order; each thread gets the sums.  In a warp, lanes that
-    // exchange several values keep half of them each time, so that eight values cost nine shuffles and end
-    // in four lanes each.  Across warps: one write, one barrier, and each lane adds its share of the warps'
+    // exchange several values keep half of them each time, so that four values cost six shuffles and end
+    // in eight lanes each.  Across warps: one write, one barrier, and each lane adds its share of the warps'
     // values.  Consecutive sums use the scratch's halves in turn: before a thread can write a half again,
     // every thread has passed the other half's barrier and so has read this one.
     template <int N>
     __device__ __forceinline__ void sum(float (&v)[N]) {
-        static_assert(N == 1 || N == 2 || N == 4 || N == 8, "");
+        static_assert(N == 1 || N == 2 || N == 4, "");
         if (!WIDE) {
             for (int o = size >> 1; o > 0; o >>= 1)
 #pragma unroll
@@ -305,20 +306,15 @@ struct Team {
             }
         }
         constexpr int span = 32 / N;  // lanes a value
-        float* s = scratch + turn * (8 * 32);
+        float* s = scratch + turn * (kTeamSums * 32);
         turn ^= 1;
         if (lane % span == 0) s[lane / span * 32 + warp] = k[0];
         __syncthreads();
-        // eight float4 of warps' values a sum: one a lane, or two where a sum has four lanes
+        // eight float4 of warps' values a sum
         const float4* f = reinterpret_cast<const float4*>(s) + lane / span * 8;
-        const float4 a = f[lane & (N == 8 ? 3 : 7)];
+        const float4 a = f[lane & 7];
         k[0] = (a.x + a.y) + (a.z + a.w);
-        if (N == 8) {
-            const float4 b = f[(lane & 3) + 4];
-            k[0] += (b.x + b.y) + (b.z + b.w);
-        } else {
-            k[0] += swap(k[0], 4);
-        }
+        k[0] += swap(k[0], 4);
         k[0] += swap(k[0], 2);
         k[0] += swap(k[0], 1);
         const float all = k[0];
