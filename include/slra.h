@@ -602,7 +602,7 @@ typedef enum slra_rope_schedule { SLRA_ROPE_PER_AXIS = 0, SLRA_ROPE_SHARED = 1 }
 /*
  * RMS norm of q and k and their rotation by positions along (t, h, w), either or both:
  *   out = R(p) (x rsqrt(mean(x^2) + eps) w), pair (a, b) -> (a cos - b sin, a sin + b cos) at the angle
- *   p[axis_j] omega_j; in fp32 (angles in double), rounded once.
+ *   p[axis_j] omega_j; in fp32 (the angle as a fraction of a turn from 64-bit integers), rounded once.
  * The attention entry points rotate q and k themselves: give them the norm alone (rotate = 0).  The
  * rotation serves attention that does not (dense layers, cached keys).
  *
@@ -610,16 +610,16 @@ typedef enum slra_rope_schedule { SLRA_ROPE_PER_AXIS = 0, SLRA_ROPE_SHARED = 1 }
  *   batch, tokens, heads,    q is [batch][tokens][heads][head_dim], k the same with kv_heads (0: no k).
  *   kv_heads, head_dim       head_dim a multiple of 8, at most 256; with g = head_dim / 8 rounded up to
  *                            a power of two, heads g and kv_heads g at most 1024; batch * tokens below 2^31.
- *   T, H, W, first_token     grid positions (default; all 1): token n of every sample sits at place
- *                            first_token + n of the row-major t, h, w grid, which must hold it (and
-                           fewer than 2^31 places).
+ *   T, H, W, first_token     grid positions (default: a 1 x 1 x tokens grid from 0): token n of every
+ *                            sample sits at place first_token + n of the row-major t, h, w grid, which
+ *                            must hold it (and fewer than 2^31 places).
  *   positions,               or listed ones: device int32 [batch][tokens][3] (t, h, w), 4-B aligned,
  *   positions_stride         samples positions_stride elements apart (default 0: one list for all
  *                            samples, else at least 3 * tokens).  T, H, W and first_token are then unused.
  *   pos_offset               added to every position, within +-2^31.
  *   rope_split               rotary pairs per (t, h, w), grouped in that order; all zero (default) =
  *                            c - 2 floor(c / 3), floor(c / 3), floor(c / 3) with c = head_dim / 2.  Their
- *                            sum may be below c: later pairs are not rotated.
+ *                            sum may be below c: later pairs pass through, as all do with rotate 0.
  *   theta                    rotary base, at least 1 (default, and 0: 10000).
  *   norm                     SLRA_QK_NORM_* (default NONE); eps positive (default 1e-6).
  *   rotate                   1 (default), or 0 with a norm: the norm alone.

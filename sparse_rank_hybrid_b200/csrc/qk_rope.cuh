@@ -17,11 +17,12 @@
 // infinity's partner and lose the sign of zeros.  Rows travel through a per-thread ring of asynchronous copies
 // (rows.cuh).
 //
-// B200, back to back, against 6557 GB/s of copy rate: 75,600 tokens x 2 x 40 heads of 128, bf16, norm per
-// head: forward 0.48-0.51 ms (93-98%), backward 0.86-0.87 ms (81-82%); 32,760 x 2 x 12 heads, norm over the
-// heads: forward out of a fused projection 76 us (81%), backward from fp32 gradients 147 us (83%).  What
-// keeps the backward and the short rows from the rate is issue: 202 to 246 instructions a warp and vector in
-// the backward, 110 to 129 in the forward.
+// B200, back to back, against 6557 GB/s of copy rate, over cards and places of the buffers: 75,600 tokens x 2 x
+// 40 heads of 128, bf16, norm per head: forward 0.47-0.54 ms (87-99%), backward 0.86-0.94 ms (75-82%); 32,760 x
+// 2 x 12 heads, norm over the heads: forward out of a fused projection 76-79 us (78-81%), backward from fp32
+// gradients 146-159 us (77-84%); the same norms without the rotation 0.47-0.51 and 0.83-0.87 ms, 72-76 and
+// 137-140 us.  What keeps the backward and the short rows from the rate is issue: 202 to 246 instructions a
+// warp and vector in the backward, 110 to 129 in the forward.
 #pragma once
 
 #include <algorithm>

@@ -26,13 +26,13 @@
 //
 // Where every row has its own modulation vectors (TOKEN: per-token modulation, single tokens) those would be
 // loaded and waited for in each row: they travel through the ring with it instead, their gradients are written
-// as the row is, and the accumulators hold the weights' sums (60,983 x 392 with an fp32 stream and affine norm,
-// backward: 676 -> 189 us; 18,550 x 3 x 1128 in fp32: 1555 -> 677; 7716 x 5 x 5016 forward: 841 -> 597), even
-// where the ring then has one stage only.  One stage of the widest rows, all in fp32, always fits (192 KB).
+// as the row is, and the accumulators hold the weights' sums (60,983 x 392 with an fp32 stream, backward with an
+// affine norm: 676 -> 200 us), even where the ring then has one stage only.  One stage of the widest rows, all in fp32, always fits (192 KB).
 //
-// B200, back to back, against 6557 GB/s of copy rate: 75,600 x 5120 bf16 forward 0.48-0.52 ms (92-98%),
-// backward 0.73-0.79 ms (90-97%); 32,760 x 1536 with an fp32 stream forward 109 us (85%), backward with
-// a modulation row per frame and an affine norm 184-189 us (73-75%).
+// B200, back to back, against 6557 GB/s of copy rate, over cards and places of the buffers: 75,600 x 5120 bf16
+// forward 0.48-0.52 ms (91-99%), backward 0.73-0.85 ms (83-97%); 32,760 x 1536 with an fp32 stream forward
+// 108-110 us (84-85%), backward with a modulation row per frame and an affine norm 184-189 us (73-75%), with the
+// norm behind the block 165 us (84%), with vectors for each token 343 us (94%).
 #pragma once
 
 #include <algorithm>
@@ -251,7 +251,8 @@ __global__ void __launch_bounds__(WIDE ? fwd_threads(V) : 128, WIDE ? 1 : kFwdNa
         async_commit();
     };
     // A stage of rows with vectors of their own is large: filled again as soon as it is read, one more row is in
-    // flight (41,854 x 4624 fp16 with fp32 vectors: 829 -> 591 us).  Else that is slower (720p: 515 -> 555).
+    // flight.  41,854 x 4624 fp16 with fp32 vectors, affine: without y 825 -> 583 us, with y and its norm 1219 ->
+    // 968, not affine 836 and 838; up to 6% slower at 1536 channels and below.  Other rows: 720p 515 -> 555.
     for (int s = 0; s < a.stages - (TOKEN ? 0 : 1); ++s) prefetch();
 
     Vec cg[V], ca[V], cb[V];  // gate wp, w (1 + scale), b (1 + scale) + shift

@@ -1041,3 +1041,38 @@ def test_norm_slices_of_one_buffer_over_a_batch():
     assert torch.equal(out[:, 2], bwd.dx) and torch.equal(out[:, 0], bwd.dy) and (out[:, 1] == 5).all()
     slra.residual_norm_bwd(p, **s, dx_out=x_out, dh=h, dx=x_out, dy=h)
     assert torch.equal(x_out, bwd.dx) and torch.equal(h, bwd.dy)
+
+
+@pytest.mark.parametrize("schedule", [slra.ROPE_PER_AXIS, slra.ROPE_SHARED])
+def test_rope_angles_of_far_positions(schedule):
+    """Positions and offsets of up to 2^31 each, against angles reduced in 60 digits (a product in double is off by
+    more than the kernel here).  An angle is p times turns, turns the integer part of 2^64 omega / 2 pi: at most 2.5
+    units off with the long double powers, so 2.5 2^-32 turns at |p| = 2^32; 2^-32 turns for the lower half that is
+    dropped; the fraction's rounding to fp32, 2^-25 half turns: 1.7 2^-24 in all.  cos and sin: 2 2^-24; a product
+    and an fma of it: 2 2^-24.  Within 6 roundings of |a| + |b|."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    two_pi = Decimal("6.28318530717958647692528676655900576839433879875021164194989")
+    L, D, offset = 48, 128, (2 ** 31, -2 ** 31, 12345)
+    p, t, d = rope_inputs(1, L, 2, 1, D, FP, norm=slra.QK_NORM_NONE, schedule=schedule, pos_offset=offset, seed=60)
+    g = torch.Generator(device="cuda").manual_seed(61)
+    pos = torch.randint(-2 ** 31, 2 ** 31 - 1, (1, L, 3), generator=g, device="cuda", dtype=torch.int64).int()
+    pos[0, 0], pos[0, 1], pos[0, 2] = 2 ** 31 - 1, -2 ** 31, 0
+    c = D // 2
+    split = (c - 2 * (c // 3), c // 3, c // 3)
+    angle = []
+    for row in pos[0].tolist():
+        for ax in range(3):
+            for m in range(split[ax]):
+                power = Decimal(sum(split[:ax]) + m) / c if schedule == slra.ROPE_SHARED else Decimal(m) / split[ax]
+                turns = (row[ax] + offset[ax]) * (-power * Decimal(10000).ln()).exp() / two_pi
+                angle.append(float((turns - turns.to_integral_value()) * two_pi))
+    angle = torch.tensor(angle, dtype=torch.float64, device="cuda").view(1, L, 1, c)
+    outs = slra.qk_rope_fwd(p, t["q"], t["k"], positions=pos)
+    back = slra.qk_rope_bwd(p, t["q"], t["k"], **d, positions=pos)
+    for got, v, sgn in ((outs[0], t["q"], 1), (outs[1], t["k"], 1), (back.dq, d["dout_q"], -1), (back.dk, d["dout_k"], -1)):
+        a, b = v.double()[..., 0::2], v.double()[..., 1::2]
+        cos, sin = angle.cos(), sgn * angle.sin()
+        ref = torch.stack([a * cos - b * sin, a * sin + b * cos], -1).flatten(-2)
+        M = (a.abs() + b.abs()).repeat_interleave(2, dim=-1)
+        close(got, ref, M, "far positions", 6)
